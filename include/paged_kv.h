@@ -58,7 +58,8 @@
  *    offending tokens are skipped and, when cache->error_flags is non-NULL,
  *    the matching PKV_FLAG_* bit is OR-ed into it.  Kernels never trap.
  *  - Not done by the library: page allocation (the caller owns the pool and
- *    the table), positional encoding (K arrives post-rotary), scale choice.
+ *    the table), scale choice.  The attention and append calls take q and K
+ *    post-rotary; pkv_qk_norm_rope and paged_kv_append_rope bring them there.
  */
 #ifndef PAGED_KV_H
 #define PAGED_KV_H
@@ -137,6 +138,81 @@ int paged_kv_append(const pkv_cache* cache, const int32_t* page_table, int32_t m
                     const int32_t* seq_lens_before, const int32_t* cu_new_tokens, int32_t batch,
                     int32_t total_new_tokens, const void* k_new, const void* v_new,
                     void* stream);
+
+/*
+ * Position rotation, with optional norms of the query and key heads.  A head
+ * row x (bf16, head_dim values, computed in fp32) becomes
+ *   y = x * w / sqrt(mean(x^2) + norm_eps)      where w is given, else y = x
+ *   z_i = y_i cos - y_j sin,  z_j = y_j cos + y_i sin
+ * for the pairs (i, j) of its first rotary_dim values, (i, i + rotary_dim/2)
+ * or, interleaved, (2i, 2i + 1); the values past rotary_dim stay y.  The
+ * angles are the caller's table, so any frequency scaling fits; the caller
+ * builds it in enough precision for its far positions.  The pages take
+ * position encoding as the model's; this is the step between a projection
+ * and paged_kv_append / the attention calls.
+ */
+typedef struct pkv_rope {
+  const float* cos_sin; /* device fp32 [max_positions][rotary_dim]: rotary_dim/2 cosines,
+                           then rotary_dim/2 sines; 16-byte aligned; NULL with rotary_dim 0 */
+  int32_t max_positions;      /* rows of cos_sin */
+  int32_t rotary_dim;         /* 0 (no rotation) or a multiple of 16, <= head_dim */
+  int32_t interleaved;        /* pairs: 0 (i, i + rotary_dim/2), else (2i, 2i + 1) */
+  const float* q_norm_weight; /* device fp32 [head_dim], 16-byte aligned; NULL: no norm */
+  const float* k_norm_weight; /* the same for K */
+  float norm_eps;             /* finite, >= 0 */
+} pkv_rope;
+
+/*
+ * Norm and rotation of queries and keys, outside the cache (for
+ * paged_decode_attention_append, or a caller's own use).
+ *   q            bf16 rows [num_q_heads][head_dim] of token t at q + t * q_stride
+ *                (elements, a multiple of 8, >= num_q_heads * head_dim), 16-byte
+ *                aligned: a slice of a fused projection's output will do
+ *   k            the same for num_kv_heads
+ *   positions    int32 [tokens], row of cos_sin for each token (may be NULL
+ *                with rotary_dim 0)
+ *   q_out, k_out bf16 [tokens][heads][head_dim], 16-byte aligned; q_out may be
+ *                q itself (k_out k) where q_stride is num_q_heads * head_dim
+ *   error_flags  optional device int32
+ * Either of q and k may be left out with a head count of 0.  A token whose
+ * position lies outside [0, max_positions) is skipped, its output rows left
+ * as they were, and sets PKV_FLAG_BAD_LENGTH.
+ * Errors: PKV_ERR_HEAD_DIM, PKV_ERR_SHAPE (rotary_dim, eps, a stride too
+ * small), PKV_ERR_NULL, PKV_ERR_ALIGN, before any launch.
+ */
+int pkv_qk_norm_rope(const pkv_rope* rope, const void* q, int64_t q_stride, int32_t num_q_heads,
+                     const void* k, int64_t k_stride, int32_t num_kv_heads, int32_t head_dim,
+                     const int32_t* positions, int32_t tokens, void* q_out, void* k_out,
+                     int32_t* error_flags, void* stream);
+
+/*
+ * Paged KV append with the norm and rotation on the way: K is normalised,
+ * rotated and stored where paged_kv_append would store it, V is stored as
+ * there, and the step's queries are rotated in the same launch.  The pool
+ * formats and scales are those of paged_kv_append; a quantised K code comes
+ * from the fp32 rotated value itself, rounded once, a bf16 K is that value
+ * rounded to bf16.
+ *   k_new, v_new  token t's [num_kv_heads][head_dim] at k_new + t * k_stride
+ *                 (v_stride), strides as in pkv_qk_norm_rope
+ *   q             token t's [num_q_heads][head_dim] at q + t * q_stride, rotated
+ *                 to q_out bf16 [total_new_tokens][num_q_heads][head_dim];
+ *                 num_q_heads 0: none
+ *   positions     int32 [total_new_tokens] rows of cos_sin, or NULL: a token's
+ *                 position in the cache, seq_lens_before[b] + (t - cu_new_tokens[b])
+ *   page_table, seq_lens_before, cu_new_tokens: as in paged_kv_append.
+ *   total_new_tokens may exceed cu_new_tokens[batch] (a padded batch): the
+ *   tokens behind the last sequence are left alone, in the pools and in q_out.
+ * A token whose page entry is invalid is not stored (PKV_FLAG_BAD_PAGE, or
+ * PKV_FLAG_BAD_LENGTH past the page table) but its queries are rotated; one
+ * whose rotation position lies outside [0, max_positions) is skipped whole
+ * (PKV_FLAG_BAD_LENGTH).
+ */
+int paged_kv_append_rope(const pkv_cache* cache, const pkv_rope* rope, const int32_t* page_table,
+                         int32_t max_pages_per_seq, const int32_t* seq_lens_before,
+                         const int32_t* cu_new_tokens, int32_t batch, int32_t total_new_tokens,
+                         const void* k_new, int64_t k_stride, const void* v_new,
+                         int64_t v_stride, const void* q, int64_t q_stride, int32_t num_q_heads,
+                         void* q_out, const int32_t* positions, void* stream);
 
 /*
  * Split planning for decode (host only, no CUDA calls).  Decode runs as one

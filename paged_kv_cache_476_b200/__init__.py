@@ -8,6 +8,8 @@ or cannot load, importing this package raises.
 
 Entry points (same names as the C ABI):
     paged_kv_append                 paged store of new tokens' K/V (bf16, E4M3, INT8, FP4)
+    paged_kv_append_rope            the same with head norms and position rotation on the way
+    pkv_qk_norm_rope                head norms and position rotation outside the cache
     paged_decode_attention          split-KV decode, persistent and balanced
     paged_prefill_chunk_attention   causal prefill chunks on tcgen05
     paged_decode_workspace_bytes, paged_decode_plan, pkv_status_string
@@ -41,6 +43,8 @@ PKV_ERR_NO_PAGES = -12
 # Every symbol include/paged_kv.h declares.
 EXPORTED = (
     "paged_kv_append",
+    "pkv_qk_norm_rope",
+    "paged_kv_append_rope",
     "paged_decode_plan",
     "paged_decode_workspace_bytes",
     "paged_decode_attention",
@@ -84,6 +88,20 @@ class PkvCache(ctypes.Structure):
     ]
 
 
+class PkvRope(ctypes.Structure):
+    """Mirror of ``struct pkv_rope``."""
+
+    _fields_ = [
+        ("cos_sin", ctypes.c_void_p),
+        ("max_positions", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("q_norm_weight", ctypes.c_void_p),
+        ("k_norm_weight", ctypes.c_void_p),
+        ("norm_eps", ctypes.c_float),
+    ]
+
+
 class AllocStats(ctypes.Structure):
     """Mirror of ``struct pkv_alloc_stats``."""
 
@@ -113,6 +131,12 @@ def _load() -> ctypes.CDLL:
     cp = ctypes.POINTER(PkvCache)
     lib.paged_kv_append.argtypes = [cp, P, I32, P, P, I32, I32, P, P, P]
     lib.paged_kv_append.restype = ctypes.c_int
+    I64, rp = ctypes.c_int64, ctypes.POINTER(PkvRope)
+    lib.pkv_qk_norm_rope.argtypes = [rp, P, I64, I32, P, I64, I32, I32, P, I32, P, P, P, P]
+    lib.pkv_qk_norm_rope.restype = ctypes.c_int
+    lib.paged_kv_append_rope.argtypes = [cp, rp, P, I32, P, P, I32, I32, P, I64, P, I64, P, I64,
+                                         I32, P, P, P]
+    lib.paged_kv_append_rope.restype = ctypes.c_int
     lib.paged_decode_plan.argtypes = [I32, I32, I32, I32, I32, I32, ctypes.POINTER(I32)]
     lib.paged_decode_plan.restype = ctypes.c_int
     lib.paged_decode_workspace_bytes.argtypes = [I32, I32, I32, I32, I32, I32]
@@ -200,6 +224,49 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _rows(name: str, t: torch.Tensor) -> int:
+    """Checks bf16 rows ``[T, H, D]`` (a slice of a wider row will do): their token stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be a bfloat16 tensor [tokens, heads, head_dim]")
+    T, H, D = t.shape
+    s = t.stride()
+    if D > 1 and s[2] != 1 or H > 1 and s[1] != D:
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return s[0] if T > 1 else H * D
+
+
+def _same_device(device: torch.device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not {device}")
+
+
+def _result(name: str, t: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
+    """A result tensor: the caller's, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _dev(name, t, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _same_device(device, **{name: t})
+    return t
+
+
+def _on(device: torch.device, stream, call):
+    """``call(raw stream)`` with ``device`` and ``stream`` current, so that what
+    the call allocates belongs to the stream that uses it."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device)
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return call(torch.cuda.current_stream().cuda_stream)
+
+
 def nvfp4_pool_bytes(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int) -> int:
     """Bytes of one FP4 pool: every row's E2M1 codes (head_dim/2 bytes), then
     every row's E4M3 block scales (head_dim/16 bytes)."""
@@ -278,6 +345,157 @@ def paged_kv_append(cache: PagedKVCache, page_table, seq_lens_before, cu_new_tok
                               seq_lens_before.shape[0], T, _ptr(k_new), _ptr(v_new),
                               _stream(stream))
     _check("paged_kv_append", st)
+
+
+def rope_cos_sin(max_positions: int, rotary_dim: int, base: float = 10000.0, inv_freq=None,
+                 device="cuda") -> torch.Tensor:
+    """The table a ``Rope`` rotates by: fp32 ``[max_positions, rotary_dim]``, the
+    cosines of ``position * inv_freq`` and then the sines, computed in fp64.
+    ``inv_freq`` (``[rotary_dim / 2]``) replaces ``base ** (-2i / rotary_dim)``.
+    """
+    half = rotary_dim // 2
+    if inv_freq is None:
+        inv_freq = base ** (-torch.arange(half, dtype=torch.float64) / half)
+    inv = torch.as_tensor(inv_freq, dtype=torch.float64).to(device)
+    if inv.shape != (half,):
+        raise ValueError("inv_freq must have rotary_dim / 2 entries")
+    angle = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+class Rope:
+    """Position rotation and optional head norms of q and K (``struct pkv_rope``).
+
+    ``cos_sin`` fp32 ``[max_positions, rotary_dim]`` (see ``rope_cos_sin``; None:
+    no rotation), pairs ``(i, i + rotary_dim / 2)`` or, ``interleaved``,
+    ``(2i, 2i + 1)``.  ``q_norm_weight`` / ``k_norm_weight`` fp32 ``[head_dim]``
+    normalise a head row by its root mean square first (None: no norm).
+    """
+
+    def __init__(self, cos_sin=None, interleaved=False, q_norm_weight=None, k_norm_weight=None,
+                 norm_eps: float = 1e-6):
+        self.device = None
+        for name, t, nd in (("cos_sin", cos_sin, 2), ("q_norm_weight", q_norm_weight, 1),
+                            ("k_norm_weight", k_norm_weight, 1)):
+            if t is not None:
+                _dev(name, t, torch.float32, nd)
+                self.device = self.device or t.device
+                _same_device(self.device, **{name: t})
+        self.cos_sin, self.interleaved = cos_sin, bool(interleaved)
+        self.q_norm_weight, self.k_norm_weight = q_norm_weight, k_norm_weight
+        self.norm_eps = float(norm_eps)
+        self._c = PkvRope(None if cos_sin is None else cos_sin.data_ptr(),
+                          0 if cos_sin is None else cos_sin.shape[0],
+                          0 if cos_sin is None else cos_sin.shape[1], int(self.interleaved),
+                          None if q_norm_weight is None else q_norm_weight.data_ptr(),
+                          None if k_norm_weight is None else k_norm_weight.data_ptr(),
+                          self.norm_eps)
+
+    @property
+    def c_struct(self) -> PkvRope:
+        return self._c
+
+    def _check(self, head_dim: int, device: torch.device):
+        if self.device is not None and self.device != device:
+            raise ValueError(f"the rotation's tensors are on {self.device}, not {device}")
+        for name in ("q_norm_weight", "k_norm_weight"):
+            w = getattr(self, name)
+            if w is not None and w.shape[0] != head_dim:
+                raise ValueError(f"{name} must have head_dim = {head_dim} entries")
+
+
+def pkv_qk_norm_rope(rope: Rope, q, k, positions=None, q_out=None, k_out=None, error_flags=None,
+                     stream=None):
+    """Norm and rotate ``q`` bf16 ``[T, Hq, D]`` and ``k`` ``[T, Hkv, D]`` (either may be None).
+
+    ``positions`` int32 ``[T]`` picks each token's row of the table.  The heads
+    of a token are contiguous, tokens may lie apart (slices of a fused
+    projection).  ``q_out`` may be ``q`` itself where that is contiguous.
+    Returns ``(q_out, k_out)``; rows of tokens with a position outside the
+    table keep what they held and raise ``PKV_FLAG_BAD_LENGTH``.
+    """
+    if q is None and k is None:
+        raise ValueError("q or k must be given")
+    T, _, D = (k if q is None else q).shape
+    device = (k if q is None else q).device
+    qs = 0 if q is None else _rows("q", q)
+    ks = 0 if k is None else _rows("k", k)
+    if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != D):
+        raise ValueError("q and k must have the same tokens and head_dim")
+    if rope.cos_sin is not None:
+        _dev("positions", positions, torch.int32, 1)
+        if positions.shape[0] != T:
+            raise ValueError("positions must have one entry per token")
+    if error_flags is not None:
+        _dev("error_flags", error_flags, torch.int32)
+    rope._check(D, device)
+    _same_device(device, k=k, positions=positions, error_flags=error_flags)
+
+    def call(s):
+        qo = None if q is None else _result("q_out", q_out, q.shape, torch.bfloat16, device)
+        ko = None if k is None else _result("k_out", k_out, k.shape, torch.bfloat16, device)
+        _check("pkv_qk_norm_rope", _lib.pkv_qk_norm_rope(
+            ctypes.byref(rope.c_struct), None if q is None else q.data_ptr(), qs,
+            0 if q is None else q.shape[1], None if k is None else k.data_ptr(), ks,
+            0 if k is None else k.shape[1], D,
+            None if positions is None else positions.data_ptr(), T,
+            None if q is None else qo.data_ptr(), None if k is None else ko.data_ptr(),
+            None if error_flags is None else error_flags.data_ptr(), s))
+        return qo, ko
+
+    return _on(device, stream, call)
+
+
+def paged_kv_append_rope(cache: PagedKVCache, rope: Rope, page_table, seq_lens_before,
+                         cu_new_tokens, k_new, v_new, q=None, q_out=None, positions=None,
+                         total_new_tokens: Optional[int] = None, stream=None):
+    """Append with the norm and rotation on the way: ``paged_kv_append`` of the
+    normed and rotated ``k_new`` and of ``v_new`` (bf16 ``[T, Hkv, D]``), and the
+    same for the step's queries ``q`` ``[T, Hq, D]`` in one launch.
+
+    A token rotates by its position in the cache, or by ``positions`` int32
+    ``[T]``.  Tokens may lie apart in memory (slices of a fused projection).
+    Returns ``q_out`` bf16 ``[T, Hq, D]`` (``q`` itself may be given where it is
+    contiguous), None without ``q``.  Tokens behind ``cu_new_tokens[-1]`` (a
+    padded batch) change nothing.
+    """
+    _dev("page_table", page_table, torch.int32, 2)
+    _dev("seq_lens_before", seq_lens_before, torch.int32, 1)
+    _dev("cu_new_tokens", cu_new_tokens, torch.int32, 1)
+    ks, vs = _rows("k_new", k_new), _rows("v_new", v_new)
+    device = cache.k_pool.device
+    T = k_new.shape[0] if total_new_tokens is None else int(total_new_tokens)
+    B, D = seq_lens_before.shape[0], cache.head_dim
+    if k_new.shape != v_new.shape or tuple(k_new.shape[1:]) != (cache.num_kv_heads, D):
+        raise ValueError("k_new and v_new must be [tokens, num_kv_heads, head_dim]")
+    if page_table.shape[0] != B or cu_new_tokens.shape[0] != B + 1:
+        raise ValueError("page_table and cu_new_tokens must match seq_lens_before")
+    if T > k_new.shape[0]:
+        raise ValueError("total_new_tokens exceeds the tokens given")
+    if q is not None:
+        qs = _rows("q", q)
+        if q.shape[0] < T or q.shape[2] != D:
+            raise ValueError("q must be [tokens, q heads, head_dim]")
+    if positions is not None:
+        _dev("positions", positions, torch.int32, 1)
+        if positions.shape[0] < T:
+            raise ValueError("positions must have one entry per token")
+    rope._check(D, device)
+    _same_device(device, page_table=page_table, seq_lens_before=seq_lens_before,
+                 cu_new_tokens=cu_new_tokens, k_new=k_new, v_new=v_new, q=q, positions=positions)
+
+    def call(s):
+        out = None if q is None else _result("q_out", q_out, q.shape, torch.bfloat16, device)
+        _check("paged_kv_append_rope", _lib.paged_kv_append_rope(
+            ctypes.byref(cache.c_struct), ctypes.byref(rope.c_struct), page_table.data_ptr(),
+            page_table.shape[1], seq_lens_before.data_ptr(), cu_new_tokens.data_ptr(), B, T,
+            k_new.data_ptr(), ks, v_new.data_ptr(), vs, None if q is None else q.data_ptr(),
+            0 if q is None else qs, 0 if q is None else q.shape[1],
+            None if q is None else out.data_ptr(),
+            None if positions is None else positions.data_ptr(), s))
+        return out
+
+    return _on(device, stream, call)
 
 
 def paged_decode_plan(batch, num_kv_heads, max_seq_len, num_sms, num_ctas=0, ctas_per_sm=1):
@@ -564,12 +782,15 @@ class StepDriver:
     and page-table rows straight into one pinned host buffer, one
     host-to-device copy moves it, and the step runs ``paged_kv_append`` over
     all rows, ``paged_decode_attention`` over the decode rows and
-    ``paged_prefill_chunk_attention`` over the chunks, on one stream.
+    ``paged_prefill_chunk_attention`` over the chunks, on one stream.  With a
+    ``rope`` the step takes unrotated K and queries and appends through
+    ``paged_kv_append_rope``.
     """
 
     def __init__(self, cache: PagedKVCache, allocator: PageAllocator, max_rows: int,
-                 device="cuda"):
+                 device="cuda", rope: Optional[Rope] = None):
         self.cache, self.alloc = cache, allocator
+        self.rope = rope
         self.max_rows = int(max_rows)
         mp = allocator.max_pages_per_seq
         n = self.max_rows
@@ -582,13 +803,19 @@ class StepDriver:
         self.device = device
 
     def step(self, decode_slots, chunk_slots, chunk_lens, k_new, v_new, q_decode=None,
-             q_chunks=None, softmax_scale=None, stream=None):
+             q_chunks=None, softmax_scale=None, stream=None, q=None):
         """Run one step; returns ``(status, decode (out, lse) or None, chunks (out, lse) or None)``.
 
         ``k_new``/``v_new``: bf16 ``[T, Hkv, D]`` on the device, the decode
         rows' tokens first, then each chunk's tokens.  On PKV_ERR_NO_PAGES
         nothing is launched and the allocator is unchanged.
+
+        With the driver's ``rope``, ``k_new`` comes unrotated and ``q`` bf16
+        ``[T, Hq, D]`` holds the unrotated queries of all tokens in the same
+        order, in place of ``q_decode`` and ``q_chunks``.
         """
+        if (self.rope is None) != (q is None):
+            raise ValueError("q goes with the driver's rope, q_decode and q_chunks without one")
         nd, nc = len(decode_slots), len(chunk_slots)
         n = nd + nc
         if n == 0 or n > self.max_rows:
@@ -622,8 +849,13 @@ class StepDriver:
             d_table = d[3 * n + 1:3 * n + 1 + n * mp].view(n, mp)
             d_cu_q = d[3 * n + 1 + n * mp:]
             total = int(cu[n])
-            paged_kv_append(self.cache, d_table, d_before, d_cu, k_new, v_new,
-                            total_new_tokens=total, stream=s)
+            if self.rope is None:
+                paged_kv_append(self.cache, d_table, d_before, d_cu, k_new, v_new,
+                                total_new_tokens=total, stream=s)
+            else:
+                q = paged_kv_append_rope(self.cache, self.rope, d_table, d_before, d_cu, k_new,
+                                         v_new, q=q, total_new_tokens=total, stream=s)
+                q_decode, q_chunks = q[:nd], q[nd:total]
             dec = chk = None
             if nd:
                 dec = paged_decode_attention(self.cache, q_decode, d_table[:nd], d_after[:nd],

@@ -127,6 +127,61 @@ static int decode_ctas_per_sm(int head_dim, int fmt, int group, int* out) {
   return PKV_OK;
 }
 
+// Where an append stores: the pools and the page geometry.
+static void fill_append(const pkv_cache* cache, const int32_t* page_table,
+                        int32_t max_pages_per_seq, const int32_t* seq_lens_before,
+                        const int32_t* cu_new_tokens, int32_t batch, AppendParams* p) {
+  p->k_pool = static_cast<uint8_t*>(cache->k_pool);
+  p->v_pool = static_cast<uint8_t*>(cache->v_pool);
+  p->k_blocks = fp4(cache->kv_dtype) ? p->k_pool + block_region_offset(cache) : nullptr;
+  p->v_blocks = fp4(cache->kv_dtype) ? p->v_pool + block_region_offset(cache) : nullptr;
+  p->k_scale = cache->k_scale;
+  p->v_scale = cache->v_scale;
+  p->page_table = page_table;
+  p->seq_lens_before = seq_lens_before;
+  p->cu_new = cu_new_tokens;
+  p->flags = cache->error_flags;
+  p->batch = batch;
+  p->max_pages = max_pages_per_seq;
+  p->num_pages = cache->num_pages;
+  p->page_size = cache->page_size;
+  p->num_kv_heads = cache->num_kv_heads;
+  p->head_dim = cache->head_dim;
+}
+
+// The rotation and norms of a pkv_rope, checked.
+static int check_rope(const pkv_rope* r, int32_t head_dim) {
+  if (!r) return PKV_ERR_NULL;
+  if (r->rotary_dim < 0 || r->rotary_dim > head_dim || r->rotary_dim % 16 != 0)
+    return PKV_ERR_SHAPE;
+  if (r->rotary_dim > 0) {
+    if (!r->cos_sin) return PKV_ERR_NULL;
+    if (!aligned16(r->cos_sin)) return PKV_ERR_ALIGN;
+    if (r->max_positions < 1) return PKV_ERR_SHAPE;
+  }
+  if (!aligned16(r->q_norm_weight) || !aligned16(r->k_norm_weight)) return PKV_ERR_ALIGN;
+  if (!std::isfinite(r->norm_eps) || r->norm_eps < 0.f) return PKV_ERR_SHAPE;
+  return PKV_OK;
+}
+
+// Rows [tokens][heads][head_dim] whose tokens lie `stride` elements apart.
+static int check_rows(const void* x, int64_t stride, int32_t heads, int32_t head_dim) {
+  if (!x) return PKV_ERR_NULL;
+  if (!aligned16(x) || stride % 8 != 0) return PKV_ERR_ALIGN;
+  if (stride < (int64_t)heads * head_dim) return PKV_ERR_SHAPE;
+  return PKV_OK;
+}
+
+static void fill_rope(const pkv_rope* r, RopeParams* p) {
+  p->cos_sin = r->cos_sin;
+  p->q_weight = r->q_norm_weight;
+  p->k_weight = r->k_norm_weight;
+  p->max_positions = r->max_positions;
+  p->rot = r->rotary_dim;
+  p->interleaved = r->interleaved != 0;
+  p->eps = r->norm_eps;
+}
+
 // Upper bound of decode CTAs used for workspace sizing.
 constexpr int kMaxDecodeCtasPerSm = 4;
 
@@ -136,7 +191,7 @@ using namespace pkv;
 
 extern "C" {
 
-int pkv_abi_version(void) { return (1 << 16) | 1; }
+int pkv_abi_version(void) { return (1 << 16) | 2; }
 
 const char* pkv_status_string(int status) {
   switch (status) {
@@ -171,27 +226,88 @@ int paged_kv_append(const pkv_cache* cache, const int32_t* page_table, int32_t m
   if (!aligned16(k_new) || !aligned16(v_new)) return PKV_ERR_ALIGN;
   int sms = 0;
   if ((st = device_sms(&sms))) return st;
-  AppendParams p;
-  p.k_pool = static_cast<uint8_t*>(cache->k_pool);
-  p.v_pool = static_cast<uint8_t*>(cache->v_pool);
-  p.k_blocks = fp4(cache->kv_dtype) ? p.k_pool + block_region_offset(cache) : nullptr;
-  p.v_blocks = fp4(cache->kv_dtype) ? p.v_pool + block_region_offset(cache) : nullptr;
-  p.k_scale = cache->k_scale;
-  p.v_scale = cache->v_scale;
-  p.page_table = page_table;
-  p.seq_lens_before = seq_lens_before;
-  p.cu_new = cu_new_tokens;
+  AppendParams p{};
+  fill_append(cache, page_table, max_pages_per_seq, seq_lens_before, cu_new_tokens, batch, &p);
   p.k_new = static_cast<const uint4*>(k_new);
   p.v_new = static_cast<const uint4*>(v_new);
-  p.flags = cache->error_flags;
-  p.batch = batch;
   p.total_new = total_new_tokens;
-  p.max_pages = max_pages_per_seq;
-  p.num_pages = cache->num_pages;
-  p.page_size = cache->page_size;
-  p.num_kv_heads = cache->num_kv_heads;
-  p.head_dim = cache->head_dim;
   cudaError_t e = launch_append(p, cache->kv_dtype, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int pkv_qk_norm_rope(const pkv_rope* rope, const void* q, int64_t q_stride, int32_t num_q_heads,
+                     const void* k, int64_t k_stride, int32_t num_kv_heads, int32_t head_dim,
+                     const int32_t* positions, int32_t tokens, void* q_out, void* k_out,
+                     int32_t* error_flags, void* stream) {
+  if (head_dim != 64 && head_dim != 128) return PKV_ERR_HEAD_DIM;
+  int st = check_rope(rope, head_dim);
+  if (st) return st;
+  if (tokens < 0 || num_q_heads < 0 || num_kv_heads < 0) return PKV_ERR_SHAPE;
+  if (tokens == 0 || num_q_heads + (int64_t)num_kv_heads == 0) return PKV_OK;
+  if (num_q_heads && ((st = check_rows(q, q_stride, num_q_heads, head_dim)) ||
+                      (st = check_rows(q_out, (int64_t)num_q_heads * head_dim, num_q_heads, head_dim))))
+    return st;
+  if (num_kv_heads && ((st = check_rows(k, k_stride, num_kv_heads, head_dim)) ||
+                       (st = check_rows(k_out, (int64_t)num_kv_heads * head_dim, num_kv_heads, head_dim))))
+    return st;
+  if (rope->rotary_dim && !positions) return PKV_ERR_NULL;
+  int sms = 0;
+  if ((st = device_sms(&sms))) return st;
+  RopeParams p{};
+  fill_rope(rope, &p);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.positions = positions;
+  p.tokens = tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.a.flags = error_flags;
+  cudaError_t e = launch_qk_norm_rope(p, head_dim, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int paged_kv_append_rope(const pkv_cache* cache, const pkv_rope* rope, const int32_t* page_table,
+                         int32_t max_pages_per_seq, const int32_t* seq_lens_before,
+                         const int32_t* cu_new_tokens, int32_t batch, int32_t total_new_tokens,
+                         const void* k_new, int64_t k_stride, const void* v_new,
+                         int64_t v_stride, const void* q, int64_t q_stride, int32_t num_q_heads,
+                         void* q_out, const int32_t* positions, void* stream) {
+  int st = check_cache(cache);
+  if (st) return st;
+  if ((st = check_rope(rope, cache->head_dim))) return st;
+  if (batch < 0 || total_new_tokens < 0 || max_pages_per_seq < 1 || num_q_heads < 0)
+    return PKV_ERR_SHAPE;
+  if ((st = check_table_span(cache, max_pages_per_seq))) return st;
+  if (total_new_tokens == 0 || batch == 0) return PKV_OK;
+  if (!page_table || !seq_lens_before || !cu_new_tokens) return PKV_ERR_NULL;
+  const int D = cache->head_dim, Hkv = cache->num_kv_heads;
+  if ((st = check_rows(k_new, k_stride, Hkv, D))) return st;
+  if ((st = check_rows(v_new, v_stride, Hkv, D))) return st;
+  if (num_q_heads && ((st = check_rows(q, q_stride, num_q_heads, D)) ||
+                      (st = check_rows(q_out, (int64_t)num_q_heads * D, num_q_heads, D))))
+    return st;
+  int sms = 0;
+  if ((st = device_sms(&sms))) return st;
+  RopeParams p{};
+  fill_rope(rope, &p);
+  fill_append(cache, page_table, max_pages_per_seq, seq_lens_before, cu_new_tokens, batch, &p.a);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k_new);
+  p.v = static_cast<const __nv_bfloat16*>(v_new);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.positions = positions;
+  p.tokens = total_new_tokens;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = Hkv;
+  cudaError_t e =
+      launch_append_rope(p, cache->kv_dtype, D, sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

@@ -267,19 +267,23 @@ __device__ __forceinline__ uint32_t int8_code(float y) {
   return static_cast<uint32_t>(q) & 0xffu;
 }
 
-// Codes of pool format kFmt for two bf16 values and their (page, head) scale
+// Codes of pool format kFmt for two fp32 values and their (page, head) scale
 // (low byte = first value): the IEEE fp32 quotient x / scale, then E4M3 with
 // round-to-nearest-even and satfinite, or the INT8 code above.  Every writer
 // of one-byte pools goes through here, so all write the same bytes.
 template <int kFmt>
-__device__ __forceinline__ uint16_t encode8x2(__nv_bfloat162 x, float scale) {
-  float2 f = __bfloat1622float2(x);
+__device__ __forceinline__ uint16_t encode8x2(float2 f, float scale) {
   f.x = __fdiv_rn(f.x, scale);
   f.y = __fdiv_rn(f.y, scale);
   if constexpr (kFmt == PKV_KV_INT8)
     return static_cast<uint16_t>(int8_code(f.x) | (int8_code(f.y) << 8));
   else
     return static_cast<uint16_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3));
+}
+
+template <int kFmt>
+__device__ __forceinline__ uint16_t encode8x2(__nv_bfloat162 x, float scale) {
+  return encode8x2<kFmt>(__bfloat1622float2(x), scale);
 }
 
 // Four 8-bit KV codes of format kFmt (one 32-bit word, byte 0 first) to two
@@ -330,12 +334,30 @@ __device__ __forceinline__ uint32_t e2m1_code(float y) {
   return m | (__float_as_uint(y) >> 31 << 3);
 }
 
+// Scale of one FP4 block whose largest magnitude is amax, under the (page, kv
+// head) scale s: the byte sb = e4m3_rne_satfinite(amax / fp32(6 s)) and
+// d = fp32(decode(sb) * s), the unit its values are divided by.
+__device__ __forceinline__ float nvfp4_block_unit(float amax, float s, uint32_t* sb_out) {
+  const float ratio = __fdiv_rn(amax, __fmul_rn(6.0f, s));
+  const uint32_t sb = (uint32_t)__nv_cvt_float_to_fp8(ratio, __NV_SATFINITE, __NV_E4M3);
+  __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sb, __NV_E4M3);
+  *sb_out = sb;
+  return __fmul_rn(__half2float(__half(hr)), s);
+}
+
+// The four code bytes of eight values of a block of unit d (element 2k in the
+// low nibble of byte k): code_i = e2m1(d > 0 ? fp32(x_i / d) : 0).
+__device__ __forceinline__ uint32_t nvfp4_codes8(const float* x, float d) {
+  uint32_t w = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w |= e2m1_code(d > 0.f ? __fdiv_rn(x[i], d) : 0.f) << (4 * i);
+  return w;
+}
+
 // One FP4 block: 16 bf16 values (lo = elements 0-7, hi = 8-15) under the
-// (page, kv head) scale s.  sb = e4m3_rne_satfinite(amax / fp32(6 s)) with
-// NaN ignored in amax; d = fp32(decode(sb) * s); code_i =
-// e2m1(d > 0 ? fp32(x_i / d) : 0).  Returns the 8 code bytes (element 2k in
-// the low nibble of byte k) and the block-scale byte.  Every writer of FP4
-// pools goes through here, so all write the same bytes.
+// (page, kv head) scale s, NaN ignored in amax.  Returns the 8 code bytes and
+// the block-scale byte.  Every writer of FP4 pools goes through the two
+// helpers above, so all write the same bytes.
 __device__ __forceinline__ uint2 nvfp4_encode_block(const uint4& lo, const uint4& hi, float s,
                                                     uint32_t* sb_out) {
   float x[16];
@@ -353,18 +375,8 @@ __device__ __forceinline__ uint2 nvfp4_encode_block(const uint4& lo, const uint4
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));  // fmaxf drops NaN
-  const float ratio = __fdiv_rn(amax, __fmul_rn(6.0f, s));
-  const uint32_t sb = (uint32_t)__nv_cvt_float_to_fp8(ratio, __NV_SATFINITE, __NV_E4M3);
-  __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sb, __NV_E4M3);
-  const float d = __fmul_rn(__half2float(__half(hr)), s);
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t c = e2m1_code(d > 0.f ? __fdiv_rn(x[i], d) : 0.f);
-    w[i >> 3] |= c << (4 * (i & 7));
-  }
-  *sb_out = sb;
-  return make_uint2(w[0], w[1]);
+  const float d = nvfp4_block_unit(amax, s, sb_out);
+  return make_uint2(nvfp4_codes8(x, d), nvfp4_codes8(x + 8, d));
 }
 
 // Four bytes of E2M1 code pairs to four f16x2 (exact; the low nibble of a

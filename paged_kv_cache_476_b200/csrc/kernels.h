@@ -87,7 +87,38 @@ struct DecodeParams {
   float scale_log2;  // softmax_scale * log2(e)
 };
 
+// Head norms and position rotation of q and k rows, with (launch_append_rope)
+// or without (launch_qk_norm_rope) the store of K and V into the pools.
+struct RopeParams {
+  const __nv_bfloat16* q;  // token t's heads at q + t * q_stride; null: none
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;  // append only
+  int64_t q_stride;        // elements between tokens
+  int64_t k_stride;
+  int64_t v_stride;
+  __nv_bfloat16* q_out;  // [T][Hq][D]
+  __nv_bfloat16* k_out;  // [T][Hkv][D], without append
+  const float* cos_sin;  // [max_positions][rot]: rot/2 cosines, then rot/2 sines
+  const float* q_weight;  // [D] or null: no norm
+  const float* k_weight;
+  const int32_t* positions;  // [T]; append: null = the cache position
+  int32_t tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t max_positions;
+  int32_t rot;  // rotary_dim
+  int32_t interleaved;
+  float eps;
+  // The error word, and for the append the page geometry and pools, as there
+  // (k_new, v_new and total_new are not used).
+  AppendParams a;
+};
+
 // fmt: the pool's pkv_kv_dtype
+cudaError_t launch_qk_norm_rope(const RopeParams& p, int head_dim, int num_sms,
+                                cudaStream_t stream);
+cudaError_t launch_append_rope(const RopeParams& p, int fmt, int head_dim, int num_sms,
+                               cudaStream_t stream);
 cudaError_t launch_append(const AppendParams& p, int fmt, int num_sms, cudaStream_t stream);
 cudaError_t decode_occupancy(int head_dim, int fmt, int group, int* ctas_per_sm);
 cudaError_t decode_run(int head_dim, int fmt, const CUtensorMap& tk, const CUtensorMap& tv,
