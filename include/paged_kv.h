@@ -303,6 +303,38 @@ int paged_decode_attention_append(const pkv_cache* cache, const void* q, int32_t
                                   void* stream);
 
 /*
+ * Decode attention for a batch whose sequences share prefixes: the same
+ * function as paged_decode_attention, with the pages that a group of sequences
+ * has in common read once for the group.  Group g is the sequences
+ * [cu_groups[g], cu_groups[g+1]); their page-table rows name the same pages for
+ * the first prefix_lens[g] tokens (rounded down to whole pages).  The prefix
+ * part runs on the tcgen05 tensor cores over the queries of the whole group.
+ *   cu_groups    int32 [num_groups+1], ascending, within [0, batch]
+ *                (PKV_FLAG_BAD_LENGTH otherwise, and results undefined);
+ *                sequences outside every group, groups of one, and sequences
+ *                with fewer tokens than their group's prefix are attended to on
+ *                their own; repeated entries (empty groups) may pad the array
+ *   prefix_lens  int32 [num_groups]; 0: nothing is shared
+ *                (negative: 0, with PKV_FLAG_BAD_LENGTH)
+ *   num_groups   0: paged_decode_attention
+ *   workspace    paged_decode_shared_workspace_bytes(...) bytes, 16-byte
+ *                aligned; one call at a time may use it
+ * Results equal paged_decode_attention's up to the order of summation, and are
+ * the same from run to run.  The other arguments, flags and errors are those of
+ * paged_decode_attention.
+ */
+size_t paged_decode_shared_workspace_bytes(int32_t batch, int32_t num_q_heads,
+                                           int32_t num_kv_heads, int32_t head_dim,
+                                           int32_t max_seq_len, int32_t num_groups);
+int paged_decode_attention_shared(const pkv_cache* cache, const void* q, int32_t num_q_heads,
+                                  int32_t gqa_group, const int32_t* page_table,
+                                  int32_t max_pages_per_seq, const int32_t* seq_lens,
+                                  int32_t batch, int32_t max_seq_len, const int32_t* cu_groups,
+                                  const int32_t* prefix_lens, int32_t num_groups,
+                                  float softmax_scale, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
  * Causal prefill-chunk attention over the paged cache.  Chunk c owns the
  * queries [cu_q_lens[c], cu_q_lens[c+1]) of the packed q and has seq_lens[c]
  * tokens cached AFTER its append (its own new tokens included).  Query i of a

@@ -11,6 +11,7 @@ Entry points (same names as the C ABI):
     paged_kv_append_rope            the same with head norms and position rotation on the way
     pkv_qk_norm_rope                head norms and position rotation outside the cache
     paged_decode_attention          split-KV decode, persistent and balanced
+    paged_decode_attention_shared   the same, reading prefixes that sequences share once
     paged_prefill_chunk_attention   causal prefill chunks on tcgen05
     paged_decode_workspace_bytes, paged_decode_plan, pkv_status_string
     PageAllocator                   host page allocator + in-flight step planner
@@ -54,6 +55,8 @@ EXPORTED = (
     "paged_decode_attention_noalloc",
     "paged_attention_combine",
     "paged_decode_attention_append",
+    "paged_decode_shared_workspace_bytes",
+    "paged_decode_attention_shared",
     "pkv_check_bounded_wait",
     # include/paged_kv_runtime.h: host page allocator and step planner
     "pkv_allocator_create",
@@ -147,6 +150,11 @@ def _load() -> ctypes.CDLL:
     lib.paged_decode_attention_append.argtypes = [cp, P, I32, I32, P, I32, P, I32, I32, F, P, P,
                                                   P, P, P, SZ, I32, P]
     lib.paged_decode_attention_append.restype = ctypes.c_int
+    lib.paged_decode_shared_workspace_bytes.argtypes = [I32, I32, I32, I32, I32, I32]
+    lib.paged_decode_shared_workspace_bytes.restype = SZ
+    lib.paged_decode_attention_shared.argtypes = [cp, P, I32, I32, P, I32, P, I32, I32, P, P, I32,
+                                                  F, P, P, P, SZ, P]
+    lib.paged_decode_attention_shared.restype = ctypes.c_int
     lib.paged_prefill_chunk_attention.argtypes = [cp, P, I32, I32, P, P, I32, P, I32, I32, I32,
                                                   F, P, P, P]
     lib.paged_prefill_chunk_attention.restype = ctypes.c_int
@@ -585,6 +593,71 @@ def paged_decode_attention_append(cache: PagedKVCache, q, page_table, seq_lens, 
         int(num_ctas), _stream(stream))
     _check("paged_decode_attention_append", st)
     return out, lse
+
+
+def decode_shared_workspace(cache: PagedKVCache, batch, num_q_heads, max_seq_len, num_groups):
+    """A workspace tensor for paged_decode_attention_shared; one call at a time may use it."""
+    device = cache.k_pool.device
+    with torch.cuda.device(device):
+        n = _lib.paged_decode_shared_workspace_bytes(batch, num_q_heads, cache.num_kv_heads,
+                                                     cache.head_dim, max_seq_len, num_groups)
+    if n == 0:
+        raise PagedKVError("paged_decode_shared_workspace_bytes", -2)
+    return torch.empty(int(n), dtype=torch.uint8, device=device)
+
+
+def paged_decode_attention_shared(cache: PagedKVCache, q, page_table, seq_lens, max_seq_len: int,
+                                  cu_groups, prefix_lens, softmax_scale: Optional[float] = None,
+                                  out=None, lse=None, workspace=None, want_lse: bool = True,
+                                  stream=None):
+    """Decode attention of a batch whose sequences share prefixes.
+
+    The function of ``paged_decode_attention``; the sequences ``cu_groups[g]``
+    to ``cu_groups[g + 1] - 1`` (int32 ``[G + 1]``) hold the same pages for their
+    first ``prefix_lens[g]`` tokens (int32 ``[G]``, rounded down to whole pages),
+    which are read once for the group.  Sequences outside the groups, or shorter
+    than their group's prefix, are attended to on their own.  A ``workspace``
+    (``decode_shared_workspace``) serves one call at a time.  Returns
+    ``(out bf16 [B, Hq, D], lse fp32 [B, Hq] or None)``.
+    """
+    _dev("q", q, torch.bfloat16, 3)
+    _dev("page_table", page_table, torch.int32, 2)
+    for name, t in (("seq_lens", seq_lens), ("cu_groups", cu_groups),
+                    ("prefix_lens", prefix_lens)):
+        _dev(name, t, torch.int32, 1)
+    B, Hq, D = q.shape
+    groups = prefix_lens.shape[0]
+    device = cache.k_pool.device
+    if D != cache.head_dim:
+        raise ValueError(f"q must have head_dim = {cache.head_dim}")
+    if page_table.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("page_table and seq_lens must match q")
+    if cu_groups.shape[0] != groups + 1:
+        raise ValueError("cu_groups must have one entry more than prefix_lens")
+    _same_device(device, q=q, page_table=page_table, seq_lens=seq_lens, cu_groups=cu_groups,
+                 prefix_lens=prefix_lens)
+    if workspace is not None:
+        _dev("workspace", workspace)
+        _same_device(device, workspace=workspace)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+
+    def call(s):
+        o = _result("out", out, (B, Hq, D), torch.bfloat16, device)
+        l = None
+        if lse is not None or want_lse:
+            l = _result("lse", lse, (B, Hq), torch.float32, device)
+        w = workspace
+        if w is None:
+            w = decode_shared_workspace(cache, B, Hq, int(max_seq_len), groups)
+        _check("paged_decode_attention_shared", _lib.paged_decode_attention_shared(
+            ctypes.byref(cache.c_struct), q.data_ptr(), Hq, Hq // cache.num_kv_heads,
+            page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), B, int(max_seq_len),
+            cu_groups.data_ptr(), prefix_lens.data_ptr(), groups, float(softmax_scale),
+            o.data_ptr(), None if l is None else l.data_ptr(), w.data_ptr(), w.nbytes, s))
+        return o, l
+
+    return _on(device, stream, call)
 
 
 def paged_prefill_chunk_attention(cache: PagedKVCache, q, cu_q_lens, page_table, seq_lens,

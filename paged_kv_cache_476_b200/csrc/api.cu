@@ -185,6 +185,35 @@ static void fill_rope(const pkv_rope* r, RopeParams* p) {
 // Upper bound of decode CTAs used for workspace sizing.
 constexpr int kMaxDecodeCtasPerSm = 4;
 
+// Groups of sequences that share a prefix (paged_decode_attention_shared).
+struct Groups {
+  const int32_t* cu;
+  const int32_t* prefix_lens;
+  int32_t num;
+};
+
+static size_t round16(size_t n) { return (n + 15) & ~size_t(15); }
+
+// CTAs of the prefix kernel (one per SM, no more than it can have steps) and
+// the rows of its partials; false if those do not fit int32.
+static bool prefix_plan(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                        int32_t max_seq_len, int32_t num_groups, int sms, int32_t* ctas,
+                        int32_t* rows) {
+  const double group = (double)num_q_heads / num_kv_heads;
+  const double steps = (batch * group / 128 + num_groups) * num_kv_heads *
+                       (((int64_t)max_seq_len + 127) / 128);
+  *ctas = steps < 1 ? 1 : steps < sms ? (int32_t)steps : sms;
+  const int64_t n = 2 * (int64_t)batch * num_q_heads + 256 * (int64_t)*ctas;
+  *rows = (int32_t)n;
+  return n <= INT32_MAX;
+}
+
+// Bytes of the prefix partials, behind the decode workspace.
+static size_t prefix_bytes(int32_t rows, int32_t units, int32_t head_dim) {
+  return (size_t)rows * head_dim * sizeof(float) + round16((size_t)rows * sizeof(float2)) +
+         (size_t)units * sizeof(int4);
+}
+
 }  // namespace pkv
 
 using namespace pkv;
@@ -350,14 +379,30 @@ size_t paged_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t 
   return (bytes + 255) & ~size_t(255);
 }
 
+size_t paged_decode_shared_workspace_bytes(int32_t batch, int32_t num_q_heads,
+                                           int32_t num_kv_heads, int32_t head_dim,
+                                           int32_t max_seq_len, int32_t num_groups) {
+  const size_t own = paged_decode_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim,
+                                                  max_seq_len, 0);
+  int sms = 0;
+  int32_t ctas = 0, rows = 0;
+  if (own == 0 || num_groups < 0 || (int64_t)batch * num_kv_heads > INT32_MAX || device_sms(&sms) ||
+      !prefix_plan(batch, num_q_heads, num_kv_heads, max_seq_len, num_groups, sms, &ctas, &rows))
+    return 0;
+  if (num_groups == 0) return own;
+  const size_t n = own + prefix_bytes(rows, batch * num_kv_heads, head_dim);
+  return (n + 255) & ~size_t(255);
+}
+
 // Decode, with the fused append of one new token per sequence when k_new
-// and v_new are given (both null otherwise).
+// and v_new are given (both null otherwise), or with the shared prefixes of
+// `groups` read once (null otherwise).
 static int decode_entry(const pkv_cache* cache, const void* q, int32_t num_q_heads,
                         int32_t gqa_group, const int32_t* page_table, int32_t max_pages_per_seq,
                         const int32_t* seq_lens, int32_t batch, int32_t max_seq_len,
-                        float softmax_scale, const void* k_new, const void* v_new, void* out,
-                        float* lse, void* workspace, size_t workspace_bytes, int32_t num_ctas,
-                        void* stream) {
+                        float softmax_scale, const void* k_new, const void* v_new,
+                        const Groups* groups, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, int32_t num_ctas, void* stream) {
   int st = check_cache(cache);
   if (st) return st;
   if ((st = check_group(cache, num_q_heads, gqa_group))) return st;
@@ -368,9 +413,13 @@ static int decode_entry(const pkv_cache* cache, const void* q, int32_t num_q_hea
   if (!aligned16(q) || !aligned16(out)) return PKV_ERR_ALIGN;
   if ((st = check_table_span(cache, max_pages_per_seq))) return st;
   if ((int64_t)max_seq_len > (int64_t)max_pages_per_seq * cache->page_size) return PKV_ERR_SHAPE;
-  const size_t need = paged_decode_workspace_bytes(batch, num_q_heads, cache->num_kv_heads,
-                                                   cache->head_dim, max_seq_len, num_ctas);
-  if (need == 0) return PKV_ERR_CUDA;
+  const size_t own_bytes = paged_decode_workspace_bytes(
+      batch, num_q_heads, cache->num_kv_heads, cache->head_dim, max_seq_len, num_ctas);
+  const size_t need =
+      groups ? paged_decode_shared_workspace_bytes(batch, num_q_heads, cache->num_kv_heads,
+                                                   cache->head_dim, max_seq_len, groups->num)
+             : own_bytes;
+  if (own_bytes == 0 || need == 0) return PKV_ERR_CUDA;
   if (!workspace || !aligned16(workspace) || workspace_bytes < need) return PKV_ERR_WORKSPACE;
 
   const int fmt = cache->kv_dtype;
@@ -443,7 +492,33 @@ static int decode_entry(const pkv_cache* cache, const void* q, int32_t num_q_hea
   p.num_pages = cache->num_pages;
   p.page_size = cache->page_size;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
-  cudaError_t e = decode_run(D, fmt, tk, tv, p, ctas, static_cast<cudaStream_t>(stream));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (!groups) {
+    e = decode_run(D, fmt, tk, tv, p, ctas, s);
+  } else {
+    p.cu_groups = groups->cu;
+    p.prefix_lens = groups->prefix_lens;
+    p.num_groups = groups->num;
+    SharedParams sp{};
+    sp.d = p;
+    sp.own_slots = (int32_t)slots;
+    int32_t pre_ctas = 0;
+    if (!prefix_plan(batch, num_q_heads, cache->num_kv_heads, max_seq_len, groups->num, sms,
+                     &pre_ctas, &sp.pre_rows))
+      return PKV_ERR_SHAPE;
+    uint8_t* pre = ws + own_bytes;
+    sp.pre_o = reinterpret_cast<float*>(pre);
+    pre += (size_t)sp.pre_rows * D * sizeof(float);
+    sp.pre_ml = reinterpret_cast<float2*>(pre);
+    pre += round16((size_t)sp.pre_rows * sizeof(float2));
+    sp.pre_info = reinterpret_cast<int4*>(pre);
+    CUtensorMap tq;
+    if ((st = encode_q_map(&tq, q, batch, num_q_heads, D, gqa_group))) return st;
+    e = shared_prefix_run(D, fmt, tq, tk, tv, sp, pre_ctas, s);
+    if (e == cudaSuccess) e = decode_run(D, fmt, tk, tv, p, ctas, s);
+    if (e == cudaSuccess) e = shared_merge_run(D, sp, s);
+  }
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -454,8 +529,24 @@ int paged_decode_attention(const pkv_cache* cache, const void* q, int32_t num_q_
                            void* workspace, size_t workspace_bytes, int32_t num_ctas,
                            void* stream) {
   return decode_entry(cache, q, num_q_heads, gqa_group, page_table, max_pages_per_seq, seq_lens,
-                      batch, max_seq_len, softmax_scale, nullptr, nullptr, out, lse, workspace,
-                      workspace_bytes, num_ctas, stream);
+                      batch, max_seq_len, softmax_scale, nullptr, nullptr, nullptr, out, lse,
+                      workspace, workspace_bytes, num_ctas, stream);
+}
+
+int paged_decode_attention_shared(const pkv_cache* cache, const void* q, int32_t num_q_heads,
+                                  int32_t gqa_group, const int32_t* page_table,
+                                  int32_t max_pages_per_seq, const int32_t* seq_lens,
+                                  int32_t batch, int32_t max_seq_len, const int32_t* cu_groups,
+                                  const int32_t* prefix_lens, int32_t num_groups,
+                                  float softmax_scale, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (num_groups < 0) return PKV_ERR_SHAPE;
+  if (batch > 0 && num_groups > 0 && (!cu_groups || !prefix_lens)) return PKV_ERR_NULL;
+  const Groups groups = {cu_groups, prefix_lens, num_groups};
+  return decode_entry(cache, q, num_q_heads, gqa_group, page_table, max_pages_per_seq, seq_lens,
+                      batch, max_seq_len, softmax_scale, nullptr, nullptr,
+                      num_groups > 0 ? &groups : nullptr, out, lse, workspace, workspace_bytes, 0,
+                      stream);
 }
 
 int paged_decode_attention_append(const pkv_cache* cache, const void* q, int32_t num_q_heads,
@@ -468,8 +559,8 @@ int paged_decode_attention_append(const pkv_cache* cache, const void* q, int32_t
   if (batch > 0 && (!k_new || !v_new)) return PKV_ERR_NULL;
   if (batch > 0 && (!aligned16(k_new) || !aligned16(v_new))) return PKV_ERR_ALIGN;
   return decode_entry(cache, q, num_q_heads, gqa_group, page_table, max_pages_per_seq, seq_lens,
-                      batch, max_seq_len, softmax_scale, k_new, v_new, out, lse, workspace,
-                      workspace_bytes, num_ctas, stream);
+                      batch, max_seq_len, softmax_scale, k_new, v_new, nullptr, out, lse,
+                      workspace, workspace_bytes, num_ctas, stream);
 }
 
 int paged_attention_combine(const void* parts, const float* lse_parts, int32_t num_parts,

@@ -180,6 +180,23 @@ __device__ __forceinline__ int32_t clamp_len(const DecodeParams& p, int32_t len,
   return len;
 }
 
+// Tokens this call attends to for sequence b: all of them, or, in a batch with
+// shared prefixes, those behind the prefix (the first page_offset(p, b) pages
+// of its table row), which another kernel reads once for its group.
+__device__ __forceinline__ int32_t own_len(const DecodeParams& p, int b, bool report) {
+  const int32_t len = clamp_len(p, __ldg(p.seq_lens + b), report);
+  if (!p.cu_groups) return len;
+  return len - shared_tokens(p.cu_groups, p.prefix_lens, p.num_groups, p.batch, b, len,
+                             p.page_size, p.max_pages);
+}
+
+__device__ __forceinline__ int32_t page_offset(const DecodeParams& p, int b) {
+  if (!p.cu_groups) return 0;
+  const int32_t len = clamp_len(p, __ldg(p.seq_lens + b), false);
+  return shared_tokens(p.cu_groups, p.prefix_lens, p.num_groups, p.batch, b, len, p.page_size,
+                       p.max_pages) / p.page_size;
+}
+
 // The work list counts each unit as its tiles plus kCost virtual tiles after
 // them, which load nothing: they stand for what a unit end costs the
 // consumers (a segment hand-off, and on average half a tile of idle lanes),
@@ -204,7 +221,7 @@ __device__ TilePos locate_tile(const DecodeParams& p, int64_t v, int lane) {
   int64_t run_v = 0, run_r = 0;
   for (int base = 0; base < p.batch; base += 32) {
     const int b = base + lane;
-    const int t = b < p.batch ? tiles_of<kTile>(clamp_len(p, __ldg(p.seq_lens + b), false)) : 0;
+    const int t = b < p.batch ? tiles_of<kTile>(own_len(p, b, false)) : 0;
     const int vt = t > 0 ? t + kCost : 0;  // virtual tiles of one unit of b
     int incl_v = vt, incl_r = t;
 #pragma unroll
@@ -238,7 +255,7 @@ __device__ TilePos locate_tile(const DecodeParams& p, int64_t v, int lane) {
         r.g = 0;
         do {
           ++r.b;
-        } while (r.b < p.batch && tiles_of<kTile>(clamp_len(p, __ldg(p.seq_lens + r.b), false)) == 0);
+        } while (r.b < p.batch && tiles_of<kTile>(own_len(p, r.b, false)) == 0);
       }
       return r;
     }
@@ -346,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int64_t tot = 0;
     for (int base = 0; base < p.batch; base += 32) {
       const int b = base + lane;
-      const int t = b < p.batch ? tiles_of<kTile>(clamp_len(p, __ldg(p.seq_lens + b), c == 0)) : 0;
+      const int t = b < p.batch ? tiles_of<kTile>(own_len(p, b, c == 0)) : 0;
       tot += t > 0 ? t + unit_end_cost<kFmt>() : 0;
     }
 #pragma unroll
@@ -366,14 +383,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       pt = s0.t;
       range_start = s0.xv;  // virtual index of the range's first real tile
     }
-    // Empty sequences (length 0): out = 0, lse = -inf, written by one CTA each.
-    for (int b = (int)((c * p.batch) / C); b < (int)(((c + 1) * p.batch) / C); ++b) {
-      if (clamp_len(p, __ldg(p.seq_lens + b), false) == 0) {
-        for (int i = lane; i < p.num_q_heads * D; i += 32)
-          p.out[(int64_t)b * p.num_q_heads * D + i] = __float2bfloat16(0.f);
-        if (p.lse)
-          for (int h = lane; h < p.num_q_heads; h += 32)
-            p.lse[(int64_t)b * p.num_q_heads + h] = -INFINITY;
+    // Empty sequences (length 0): out = 0, lse = -inf, written by one CTA each
+    // (with shared prefixes the merge writes every row).
+    if (!p.cu_groups) {
+      for (int b = (int)((c * p.batch) / C); b < (int)(((c + 1) * p.batch) / C); ++b) {
+        if (own_len(p, b, false) == 0) {
+          for (int i = lane; i < p.num_q_heads * D; i += 32)
+            p.out[(int64_t)b * p.num_q_heads * D + i] = __float2bfloat16(0.f);
+          if (p.lse)
+            for (int h = lane; h < p.num_q_heads; h += 32)
+              p.lse[(int64_t)b * p.num_q_heads + h] = -INFINITY;
+        }
       }
     }
     if (lane == 0) s_misc[0] = (int)n_tiles;
@@ -448,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     const int P = p.page_size;
     int b = pb, g = pg, t = pt;
-    int len = clamp_len(p, __ldg(p.seq_lens + b), false);
+    int len = own_len(p, b, false);
     int ntile = tiles_of<kTile>(len);
     int seg_first_t = t;
     // page ids (and scales) of 32 consecutive pages, one per lane
@@ -476,7 +496,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         cache_key = key;
         cache_j0 = j_first;
         const int jj = j_first + lane;
-        my_pid = jj < pages_b ? __ldg(p.page_table + (int64_t)b * p.max_pages + jj) : 0;
+        my_pid = jj < pages_b ? __ldg(p.page_table + (int64_t)b * p.max_pages +
+                                       page_offset(p, b) + jj) : 0;
         if constexpr (quant(kFmt)) {
           if (jj < pages_b && my_pid >= 0 && my_pid < p.num_pages) {
             my_ks = __ldg(p.k_scale + (int64_t)my_pid * Hkv + g);
@@ -537,7 +558,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         ti.tile = t;
         ti.valid = min(kTile, len - tok0);
         ti.flags = (first ? kSegFirst : 0) | (last ? kSegLast : 0) | hflags;
-        if (last && seg_first_t == 0 && t == ntile - 1) ti.flags |= kUnitWhole;
+        // (with shared prefixes no unit is whole: its prefix part is to come)
+        if (last && seg_first_t == 0 && t == ntile - 1 && !p.cu_groups) ti.flags |= kUnitWhole;
         if (first) {
           // once per unit: which CTAs share it, hence its partial slots
           const int64_t u = (int64_t)b * Hkv + g;
@@ -608,9 +630,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           g = 0;
           do {
             ++b;
-          } while (b < p.batch && tiles_of<kTile>(clamp_len(p, __ldg(p.seq_lens + b), false)) == 0);
+          } while (b < p.batch && tiles_of<kTile>(own_len(p, b, false)) == 0);
           if (b < p.batch) {
-            len = clamp_len(p, __ldg(p.seq_lens + b), false);
+            len = own_len(p, b, false);
             ntile = tiles_of<kTile>(len);
           }
         }
@@ -1167,7 +1189,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const DecodeParams p)
   const int b = u / p.num_kv_heads;
   const int g = u - b * p.num_kv_heads;
   const int2 info = p.unit_info[u];
-  if (clamp_len(p, __ldg(p.seq_lens + b), false) == 0) return;  // written by the decode kernel
+  if (own_len(p, b, false) == 0) return;  // written by the decode kernel
   const int n = info.y;
   if (n <= 1) return;  // whole unit: written by the decode kernel
   constexpr int GD = G * D;
@@ -1306,7 +1328,7 @@ cudaError_t run_for(const CUtensorMap& tk, const CUtensorMap& tv, const DecodePa
     case Plan::k3x2: e = decode_launch<D, kFmt, 3, 2>(tk, tv, p, num_ctas, stream); break;
     default: e = decode_launch<D, kFmt, 2, 4>(tk, tv, p, num_ctas, stream); break;
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.cu_groups) return e;  // shared prefixes: merged by their own kernel
   return merge_launch<D>(p, stream);
 }
 

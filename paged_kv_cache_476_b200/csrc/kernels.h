@@ -77,6 +77,11 @@ struct DecodeParams {
   // FP4 pools: the block-scale regions (after the codes) that the loads read
   const uint8_t* k_blocks;
   const uint8_t* v_blocks;
+  // Shared prefixes (null otherwise): the kernel then attends to each
+  // sequence's own tokens alone and leaves every result as partials.
+  const int32_t* cu_groups;    // [num_groups + 1]
+  const int32_t* prefix_lens;  // [num_groups]
+  int32_t num_groups;
   int32_t batch;
   int32_t num_q_heads;
   int32_t num_kv_heads;
@@ -85,6 +90,16 @@ struct DecodeParams {
   int32_t num_pages;
   int32_t page_size;
   float scale_log2;  // softmax_scale * log2(e)
+};
+
+// Shared-prefix attention: the partials of the prefix kernel.
+struct SharedParams {
+  DecodeParams d;    // the whole call; its partials hold the sequences' own tokens
+  float* pre_o;      // prefix partials: float4 vectors, see shared.cu
+  float2* pre_ml;    // (max, sum) of each partial row
+  int4* pre_info;    // [batch * num_kv_heads]: where a unit's prefix partials are
+  int32_t pre_rows;  // rows that pre_o and pre_ml hold
+  int32_t own_slots; // partial slots of d (of group rows each)
 };
 
 // Head norms and position rotation of q and k rows, with (launch_append_rope)
@@ -124,6 +139,14 @@ cudaError_t decode_occupancy(int head_dim, int fmt, int group, int* ctas_per_sm)
 cudaError_t decode_run(int head_dim, int fmt, const CUtensorMap& tk, const CUtensorMap& tv,
                        const DecodeParams& p, int num_ctas, cudaStream_t stream);
 
+// The prefix kernel with num_ctas CTAs (tq: 3-D map of the queries; tk, tv:
+// maps of the pools with boxes of 64 rows), and the merge of its partials with
+// those of the sequences' own tokens.
+cudaError_t shared_prefix_run(int head_dim, int fmt, const CUtensorMap& tq, const CUtensorMap& tk,
+                              const CUtensorMap& tv, const SharedParams& p, int num_ctas,
+                              cudaStream_t stream);
+cudaError_t shared_merge_run(int head_dim, const SharedParams& p, cudaStream_t stream);
+
 cudaError_t launch_combine(const void* parts, const float* lse_parts, int num_parts, int rows,
                            int head_dim, void* out, float* lse, cudaStream_t stream);
 
@@ -133,6 +156,7 @@ int check_table_span(const pkv_cache* c, int32_t max_pages_per_seq);
 int64_t block_region_offset(const pkv_cache* c);
 int encode_pool_map(CUtensorMap* map, void* base, bool bytes, int64_t rows, int row_elems,
                     int box_cols, int box_rows);
+int encode_q_map(CUtensorMap* map, const void* q, int total_q, int hq, int d, int group);
 int prefill_entry(const pkv_cache* cache, const void* q, int32_t num_q_heads, int32_t gqa_group,
                   const int32_t* cu_q_lens, const int32_t* page_table, int32_t max_pages_per_seq,
                   const int32_t* seq_lens, int32_t num_chunks, int32_t total_q,

@@ -1,0 +1,891 @@
+// Decode attention for a batch whose sequences share long prefixes (sm_100a,
+// tcgen05): the prefix part and the merge.
+//
+// What it computes: paged_decode_attention's function, for groups of
+// sequences whose first tokens are the same pages.  Softmax over a union of
+// key sets is the sum of the sets' parts,
+//   M = max_i m_i,  out = sum_i e^(m_i - M) o_i / sum_i e^(m_i - M) l_i,
+// with m_i, l_i = sum e^(s - m_i), o_i = sum e^(s - m_i) v over part i.  So
+// the queries of a whole group (n sequences x G heads of a kv head) attend to
+// the prefix together, one read of its K and V for all, the decode kernel
+// attends to each sequence's own tokens, and a merge adds the parts up.
+//
+// The prefix kernel.
+//  * Bound: HBM bytes of the prefix up to about 250 rows (n * G) of bf16, the
+//    tensor cores and the softmax above that.
+//  * Items.  A group's rows of one kv head are cut into pairs of 128-row Q
+//    tiles, A and B.  An item is (group, kv head, pair) over the prefix's
+//    128-key tiles.  The items' steps (a tile times one Q tile) in order are
+//    split into equal ranges, one per CTA (one CTA per SM), as decode splits
+//    its work list; a range's part of an item is a segment, whose (m, l, o)
+//    goes to the workspace.
+//  * An item with one Q tile alternates the key tiles between the two
+//    accumulators (slot 0 the even ones, slot 1 the odd), so that one slot's
+//    softmax runs under the other's products there too; both slots leave
+//    partials.
+//  * Roles as in the prefill kernel: warps 0-3 and 4-7 softmax of slot 0 and 1,
+//    one TMEM lane a row; warp 8 loads (Q by a 3-D map, K and V tiles page by
+//    page into two-slot rings); warp 9 issues the MMAs, S = Q K^T and
+//    O += P V with P from TMEM; two warps convert quantised tiles.  Step i
+//    belongs to slot i & 1 whatever the mode: step i's PV, then step i + 2's S.
+//  * The segments of a CTA run one after the other between barriers; rings and
+//    phases carry on across them.
+//  * Quantised K and V: codes convert exactly to 16 bits; the K scales multiply
+//    the scores of their 64-key block, the V scales ride on P.
+//  * Every wait is bounded; a timeout ends the CTA with the error flag set.
+#include <mutex>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tensor.cuh"
+
+namespace pkv {
+
+namespace sh {
+
+using namespace pf;
+
+constexpr int kStages = 2;     // K/V ring depth
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kConvWarp0 = 10;
+constexpr int kConvWarps = 2;
+constexpr int kConvThreads = kConvWarps * 32;
+// A facts slot is refilled when tile j - 2 has left the K ring.  With one Q
+// tile the softmax of tile j - 4 may still run then (the converters are ahead
+// of the products), so eight slots.
+constexpr int kFactsRing = 8;
+constexpr int kPairRows = 2 * kRows;
+constexpr int kMaxSegments = 1 << 16;     // more than any GPU has SMs
+constexpr float kTiny = 1.17549435e-38f;       // smallest normal fp32
+constexpr float kSumUnit = 1.f / (1ull << 60);  // unit of l for quantised pools
+
+struct TileFacts {
+  int32_t bad;  // bit per 64-key block: rejected page
+  float ks[2];  // K scales of the blocks' pages
+  float vs[2];  // V scales
+};
+
+// One CTA's part of an item.
+struct Segment {
+  int32_t b0, b1;        // sequences of the item
+  int32_t b_table;       // sequence whose table row holds the prefix's pages
+  int32_t head;
+  int32_t rows;          // (b1 - b0) * G
+  int32_t prefix;        // tokens
+  int32_t tile0, tile1;  // key tiles of the segment
+  int32_t row_base;      // first partial row of the segment
+};
+
+template <int D, int kFmt>
+struct Smem {
+  static constexpr int kHalves = D / 64;        // 128-byte column boxes per bf16 row
+  static constexpr int kQB = kRows * D * 2;     // one Q tile
+  static constexpr int kTileB = kKeys * D * 2;  // bf16 K (or V) tile
+  static constexpr int kHalfB = kKeys * 128;    // one 64-column half of a bf16 tile
+  static constexpr int kCodeRowB = row_code_bytes(kFmt, D);
+  static constexpr int kScaleRowB = row_scale_bytes(kFmt, D);
+  static constexpr int kCodesB = kKeys * kCodeRowB;
+  static constexpr int kTileQB = kCodesB + kKeys * kScaleRowB;
+  static constexpr int kStageB = quant(kFmt) ? 2 * kTileQB : 2 * kTileB;
+  static constexpr int kConvB = quant(kFmt) ? 2 * kTileB : 0;  // converted K, then V
+  static constexpr int kBytes = 2 * kQB + kStages * kStageB + kConvB;
+  static constexpr int kThreads = (quant(kFmt) ? kConvWarp0 + kConvWarps : kConvWarp0) * 32;
+};
+
+// Barriers and small state behind the tiles.
+struct Control {
+  uint64_t q_full;
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t s_full[2], p_full[2], o_bar[2];
+  uint64_t done_bar;
+  uint64_t kc_full, kc_free, vc_full, vc_free;
+  uint64_t facts_full[kFactsRing];
+  TileFacts facts[kFactsRing];
+  Segment seg;
+  int32_t more;   // a segment is in `seg`
+  int32_t abort;  // a wait gave up
+  uint32_t tmem;
+};
+
+// ---------------------------------------------------------------- work list
+struct GroupWork {
+  int32_t b0, b1, prefix, tiles, q_tiles;  // q_tiles of 128 rows
+  int64_t steps;                           // of one kv head
+};
+
+__device__ __forceinline__ GroupWork group_work(const DecodeParams& p, int g) {
+  GroupWork w;
+  w.b0 = __ldg(p.cu_groups + g);
+  w.b1 = __ldg(p.cu_groups + g + 1);
+  w.prefix = group_tokens(p.cu_groups, p.prefix_lens, g, p.batch, p.page_size, p.max_pages);
+  w.tiles = (w.prefix + kKeys - 1) / kKeys;
+  w.q_tiles = w.prefix > 0 ? ((w.b1 - w.b0) * p.group + kRows - 1) / kRows : 0;
+  w.steps = (int64_t)w.tiles * w.q_tiles;
+  return w;
+}
+
+// First CTA whose range [c*T/C, (c+1)*T/C) reaches past step x.
+__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t C, int64_t T) {
+  return ((x + 1) * C - 1) / T;
+}
+
+// Position in the work list: group, head, pair of Q tiles, key tile.
+struct Cursor {
+  GroupWork w;
+  int32_t g, head, pair, tile;
+  int64_t item_x;  // step index of the item's first step
+};
+
+// Q tiles of a group's pair.
+__device__ __forceinline__ int pair_tiles(const GroupWork& w, int pair) {
+  return min(2, w.q_tiles - 2 * pair);
+}
+
+// Warp-wide: the tile that step x belongs to (x < T); tiles go to the range
+// that holds their last step.
+__device__ Cursor locate(const DecodeParams& p, int64_t x, int lane) {
+  Cursor c;
+  int64_t run = 0;
+  for (int base = 0; base < p.num_groups; base += 32) {
+    const int g = base + lane;
+    const int64_t s = g < p.num_groups ? group_work(p, g).steps * p.num_kv_heads : 0;
+    int64_t incl = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
+    if (run + all > x) {
+      const int l0 = __ffs(__ballot_sync(0xffffffffu, run + incl > x)) - 1;
+      const int64_t before = run + __shfl_sync(0xffffffffu, incl - s, l0);
+      c.g = base + l0;
+      c.w = group_work(p, c.g);
+      int64_t off = x - before;
+      c.head = (int)(off / c.w.steps);
+      off -= c.head * c.w.steps;
+      c.pair = (int)(off / (2 * (int64_t)c.w.tiles));
+      off -= c.pair * 2 * (int64_t)c.w.tiles;
+      c.tile = (int)(off / pair_tiles(c.w, c.pair));
+      c.item_x = x - off;
+      return c;
+    }
+    run += all;
+  }
+  c.g = p.num_groups;  // not reached for x < T
+  c.w = GroupWork{};
+  c.head = c.pair = c.tile = 0;
+  c.item_x = run;
+  return c;
+}
+
+// Steps of all items.  Warp-wide.
+__device__ int64_t total_steps(const DecodeParams& p, int lane) {
+  int64_t t = 0;
+  for (int g = lane; g < p.num_groups; g += 32) t += group_work(p, g).steps;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t * p.num_kv_heads;
+}
+
+// First sequence of a group that holds the whole prefix, whose table row names
+// the prefix's pages; -1: none does.  Warp-wide.
+__device__ int first_holder(const DecodeParams& p, const GroupWork& w, int lane) {
+  for (int base = w.b0; base < w.b1; base += 32) {
+    const int b = base + lane;
+    const uint32_t hit =
+        __ballot_sync(0xffffffffu, b < w.b1 && __ldg(p.seq_lens + min(b, w.b1 - 1)) >= w.prefix);
+    if (hit) return base + __ffs(hit) - 1;
+  }
+  return -1;
+}
+
+template <int D, int kFmt>
+__global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                  const __grid_constant__ CUtensorMap tmap_k,
+                  const __grid_constant__ CUtensorMap tmap_v, const SharedParams sp) {
+  using Sm = Smem<D, kFmt>;
+  const DecodeParams& p = sp.d;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sq = smem;                            // Q tile A, then Q tile B
+  uint8_t* skv = smem + 2 * Sm::kQB;             // stage s: K at s*kStageB, V after it
+  uint8_t* sconv = skv + kStages * Sm::kStageB;  // quantised: 16-bit K, then V
+  Control& ct = *reinterpret_cast<Control*>(smem + Sm::kBytes);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int G = p.group;
+  const int TQ = kRows / G;  // sequences per Q tile
+
+  // ------------------------------------------------ this CTA's range (warp 0)
+  int64_t T = 0, Ce = 1, x_end = 0;
+  Cursor cur{};
+  bool more = false;  // warp 0: `cur` is a segment to run
+  if (warp == 0) {
+    T = total_steps(p, lane);
+    // two steps a CTA at least, so that every range holds a whole tile
+    Ce = min((int64_t)gridDim.x, T / 2);
+    if (Ce < 1) Ce = 1;
+    const int64_t c = blockIdx.x;
+    more = c < Ce && T > 0;
+    if (more) {
+      cur = locate(p, c * T / Ce, lane);
+      x_end = (c + 1) * T / Ce;
+    }
+    if (lane == 0) {
+      ct.more = more ? 1 : 0;
+      ct.abort = 0;
+    }
+    if (c == 0)
+      for (int g = lane; g < p.num_groups; g += 32) {
+        const int32_t b0 = __ldg(p.cu_groups + g), b1 = __ldg(p.cu_groups + g + 1);
+        if (b0 < 0 || b1 < b0 || b1 > p.batch || __ldg(p.prefix_lens + g) < 0)
+          flag_error(p.flags, PKV_FLAG_BAD_LENGTH);
+      }
+  }
+  if (warp == 1 && lane == 0) {
+    mbar_init(&ct.q_full, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&ct.k_full[s], 1);
+      mbar_init(&ct.v_full[s], 1);
+      // quantised: released by the converter warps
+      mbar_init(&ct.k_empty[s], quant(kFmt) ? kConvWarps : 1);
+      mbar_init(&ct.v_empty[s], quant(kFmt) ? kConvWarps : 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&ct.s_full[x], 1);
+      mbar_init(&ct.p_full[x], 4);
+      mbar_init(&ct.o_bar[x], 1);
+    }
+    mbar_init(&ct.done_bar, 1);
+    mbar_init(&ct.kc_full, kConvWarps);
+    mbar_init(&ct.kc_free, 1);
+    mbar_init(&ct.vc_full, kConvWarps);
+    mbar_init(&ct.vc_free, 1);
+    for (int s = 0; s < kFactsRing; ++s) mbar_init(&ct.facts_full[s], 1);
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(&ct.tmem, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ct.tmem;
+
+  // Carried across segments: key tiles and Q loads so far (every role counts
+  // the same), and the steps of each slot.
+  uint32_t jbase = 0, nseg = 0;
+  uint32_t cbase[2] = {0, 0};
+
+  while (true) {
+    // -------------------------------------------------- the next segment
+    const int b_table = more ? first_holder(p, cur.w, lane) : -1;
+    if (more && lane == 0) {
+      const int w = pair_tiles(cur.w, cur.pair);
+      Segment s;
+      s.b0 = cur.w.b0 + cur.pair * 2 * TQ;
+      s.b1 = min(cur.w.b1, s.b0 + 2 * TQ);
+      s.b_table = b_table;
+      s.head = cur.head;
+      s.rows = (s.b1 - s.b0) * G;
+      s.prefix = cur.w.prefix;
+      s.tile0 = cur.tile;
+      // tiles whose last step lies before the range's end
+      s.tile1 = (int)min((int64_t)cur.w.tiles, (x_end - cur.item_x) / w);
+      if (b_table < 0) s.tile1 = s.tile0;  // nobody to read the result
+      const int64_t base = 2 * ((int64_t)p.num_kv_heads * cur.w.b0 * G +
+                                (int64_t)cur.head * (cur.w.b1 - cur.w.b0) * G +
+                                (int64_t)cur.pair * kPairRows);
+      const int64_t row = base + (int64_t)kPairRows * blockIdx.x;
+      // Items of one CTA lie 2 * rows apart, parts of an item kPairRows: no two
+      // segments overlap, and the last ends by 2 * batch * heads + kPairRows * CTAs.
+      s.row_base = (int32_t)row;
+      if (s.tile0 == 0 && s.tile1 > 0) {
+        const int64_t c0 = cta_of(cur.item_x + w - 1, Ce, T);
+        const int64_t c1 = cta_of(cur.item_x + (int64_t)cur.w.tiles * w - 1, Ce, T);
+        const int4 info =
+            make_int4((int)(base + kPairRows * c0), (int)(c1 - c0 + 1), s.b0, s.rows);
+        for (int b = s.b0; b < s.b1; ++b)
+          sp.pre_info[(int64_t)b * p.num_kv_heads + s.head] = info;
+      }
+      ct.seg = s;
+    }
+    __syncthreads();
+    if (!ct.more || ct.abort) break;
+    const Segment sg = ct.seg;
+    const int n = max(sg.tile1 - sg.tile0, 0);     // key tiles
+    const bool pairs = sg.rows > kRows;            // two Q tiles
+    const int nsteps = pairs ? 2 * n : n;
+    const int steps_x[2] = {(nsteps + 1) >> 1, nsteps >> 1};
+    bool ok = true;
+
+    if (n > 0 && warp == kProducerWarp) {
+      // ---------------------------------------------------------- producer
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&ct.q_full, (uint32_t)(pairs ? 2 : 1) * Sm::kQB);
+        for (int x = 0; x < (pairs ? 2 : 1); ++x)
+#pragma unroll
+          for (int h = 0; h < Sm::kHalves; ++h)
+            tma_load_3d(sq + x * Sm::kQB + h * (kRows * 128), &tmap_q, h * 64, sg.head * G,
+                        sg.b0 + x * TQ, &ct.q_full);
+        const uint64_t pol = policy_evict_first();
+        // bytes of one operand (K or V) per live 64-key block
+        constexpr uint32_t kBlockBytes =
+            quant(kFmt) ? 64u * (Sm::kCodeRowB + Sm::kScaleRowB) : Sm::kHalves * 64u * 128u;
+        for (int i = 0; i < n; ++i) {
+          const uint32_t j = jbase + i;
+          const int st = j % kStages;
+          const uint32_t ph = (j / kStages - 1) & 1;
+          // page lookup: page ids, scales, rejected 64-key blocks
+          TileFacts tf;
+          tf.bad = 0;
+          int live = 0;
+          int32_t ys[2] = {0, 0};
+          for (int sb = 0; sb < 2; ++sb) {
+            tf.ks[sb] = tf.vs[sb] = 1.f;
+            const int32_t key0 = (sg.tile0 + i) * kKeys + sb * 64;
+            if (key0 >= sg.prefix) continue;
+            const int32_t pid =
+                __ldg(p.page_table + (int64_t)sg.b_table * p.max_pages + key0 / p.page_size);
+            if (pid < 0 || pid >= p.num_pages) {
+              flag_error(p.flags, PKV_FLAG_BAD_PAGE);
+              tf.bad |= 1 << sb;
+              continue;
+            }
+            if constexpr (quant(kFmt)) {
+              const float ks = __ldg(p.k_scale + (int64_t)pid * p.num_kv_heads + sg.head);
+              const float vs = __ldg(p.v_scale + (int64_t)pid * p.num_kv_heads + sg.head);
+              if (!(ks > 0.f && ks <= 32768.f && vs > 0.f && vs <= 32768.f)) {
+                flag_error(p.flags, PKV_FLAG_BAD_SCALE);
+                tf.bad |= 1 << sb;
+                continue;
+              }
+              tf.ks[sb] = ks;
+              tf.vs[sb] = vs;
+            }
+            ys[sb] = (int32_t)(((int64_t)pid * p.num_kv_heads + sg.head) * p.page_size +
+                               key0 % p.page_size);
+            live |= 1 << sb;
+          }
+          auto load = [&](const CUtensorMap* map, const uint8_t* blocks, uint8_t* dst,
+                          uint64_t* bar) {
+            mbar_arrive_expect_tx(bar, (uint32_t)__popc(live) * kBlockBytes);
+            for (int sb = 0; sb < 2; ++sb) {
+              if (!((live >> sb) & 1)) continue;
+              if constexpr (quant(kFmt)) {
+                tma_load_2d(dst + sb * 64 * Sm::kCodeRowB, map, 0, ys[sb], bar, pol);
+                if constexpr (fp4(kFmt))
+                  bulk_load(dst + Sm::kCodesB + sb * 64 * Sm::kScaleRowB,
+                            blocks + (int64_t)ys[sb] * Sm::kScaleRowB, 64u * Sm::kScaleRowB, bar);
+              } else {
+#pragma unroll
+                for (int h = 0; h < Sm::kHalves; ++h)
+                  tma_load_2d(dst + h * Sm::kHalfB + sb * 64 * 128, map, h * 64, ys[sb], bar,
+                              pol);
+              }
+            }
+          };
+          uint8_t* kd = skv + st * Sm::kStageB;
+          if (j >= kStages && !mbar_wait(&ct.k_empty[st], ph, p.flags)) { ok = false; break; }
+          ct.facts[j % kFactsRing] = tf;
+          mbar_arrive(&ct.facts_full[j % kFactsRing]);
+          load(&tmap_k, p.k_blocks, kd, &ct.k_full[st]);
+          if (j >= kStages && !mbar_wait(&ct.v_empty[st], ph, p.flags)) { ok = false; break; }
+          load(&tmap_v, p.v_blocks, kd + Sm::kStageB / 2, &ct.v_full[st]);
+        }
+        // every load has landed before the segment ends (the CTA may end then)
+        for (int i = max(0, n - kStages); i < n && ok; ++i) {
+          const uint32_t j = jbase + i;
+          ok = mbar_wait(&ct.k_full[j % kStages], (j / kStages) & 1, p.flags) &&
+               mbar_wait(&ct.v_full[j % kStages], (j / kStages) & 1, p.flags);
+        }
+        if (!ok) ct.abort = 1;
+      }
+    } else if (n > 0 && quant(kFmt) && warp >= kConvWarp0) {
+      // -------------------------------------------- codes -> 16-bit converters
+      const int t = threadIdx.x - kConvWarp0 * 32;
+      const uint32_t kc = smem_u32(sconv), vc = kc + Sm::kTileB;
+      for (int i = 0; i < n; ++i) {
+        const uint32_t j = jbase + i;
+        const int st = j % kStages;
+        const uint32_t par = (j / kStages) & 1;
+        if (!mbar_wait(&ct.k_full[st], par, p.flags)) { ok = false; break; }
+        const uint32_t k_codes = smem_u32(skv + st * Sm::kStageB);
+        const uint32_t v_codes = k_codes + Sm::kStageB / 2;
+        const int bad = ct.facts[j % kFactsRing].bad;
+        const int32_t key0 = (sg.tile0 + i) * kKeys;
+        const int zero_from = key0 + kKeys > sg.prefix ? max(0, sg.prefix - key0) : kKeys;
+        if (j >= 1 && !mbar_wait(&ct.kc_free, (j - 1) & 1, p.flags)) { ok = false; break; }
+        if constexpr (fp4(kFmt))
+          convert_fp4_tile<D, false, kConvThreads>(k_codes, kc, t, zero_from, bad);
+        else
+          convert_tile<D, kFmt, false, kConvThreads>(k_codes, kc, t, zero_from, bad);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ct.kc_full);
+          mbar_arrive(&ct.k_empty[st]);
+        }
+        if (!mbar_wait(&ct.v_full[st], par, p.flags)) { ok = false; break; }
+        if (j >= 1 && !mbar_wait(&ct.vc_free, (j - 1) & 1, p.flags)) { ok = false; break; }
+        if constexpr (fp4(kFmt))
+          convert_fp4_tile<D, true, kConvThreads>(v_codes, vc, t, zero_from, bad);
+        else
+          convert_tile<D, kFmt, true, kConvThreads>(v_codes, vc, t, zero_from, bad);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ct.vc_full);
+          mbar_arrive(&ct.v_empty[st]);
+        }
+      }
+      if (!ok) ct.abort = 1;
+    } else if (n > 0 && warp == kMmaWarp) {
+      // --------------------------------------------------------------- MMA
+      const uint32_t id_s = idesc_f16kind(kRows, kKeys, 0, true);
+      const uint32_t id_o = idesc_f16kind(kRows, D, 1, !quant(kFmt));
+      const uint32_t q_addr = smem_u32(sq);
+      ok = mbar_wait(&ct.q_full, nseg & 1, p.flags);
+      // local tile of step s, and whether the step is its tile's first / last
+      auto tile_of = [&](int s) { return pairs ? s >> 1 : s; };
+      auto first_of = [&](int s) { return !pairs || !(s & 1); };
+      auto last_of = [&](int s) { return !pairs || (s & 1); };
+      uint32_t k_addr = 0, v_addr = 0;
+      // S of step s: wait for its K tile, issue, release the tile after its last step
+      auto issue_s = [&](int s) -> bool {
+        const uint32_t j = jbase + tile_of(s);
+        if (first_of(s)) {
+          if constexpr (quant(kFmt)) {
+            k_addr = smem_u32(sconv);
+            if (!mbar_wait(&ct.kc_full, j & 1, p.flags)) return false;
+          } else {
+            k_addr = smem_u32(skv + (j % kStages) * Sm::kStageB);
+            if (!mbar_wait(&ct.k_full[j % kStages], (j / kStages) & 1, p.flags)) return false;
+          }
+        }
+        const int x = s & 1;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t qa = q_addr + (pairs ? x * Sm::kQB : 0);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const int h = kk >> 2, w = kk & 3;
+            const uint64_t ad = sdesc(qa + h * (kRows * 128) + w * 32, 16, 1024);
+            const uint64_t bd = sdesc(k_addr + h * Sm::kHalfB + w * 32, 16, 1024);
+            mma_ss(tmem + col_s(x), ad, bd, id_s, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&ct.s_full[x]);
+          if (last_of(s)) tc_commit(quant(kFmt) ? &ct.kc_free : &ct.k_empty[j % kStages]);
+        }
+        __syncwarp();
+        return true;
+      };
+      // O += P V of step s; V rows past the end or of a rejected page are zeroed
+      auto issue_pv = [&](int s) -> bool {
+        const uint32_t j = jbase + tile_of(s);
+        if (first_of(s)) {
+          if constexpr (quant(kFmt)) {
+            v_addr = smem_u32(sconv) + Sm::kTileB;
+            if (!mbar_wait(&ct.vc_full, j & 1, p.flags)) return false;
+          } else {
+            const int st = j % kStages;
+            if (!mbar_wait(&ct.v_full[st], (j / kStages) & 1, p.flags)) return false;
+            const int32_t key0 = (sg.tile0 + tile_of(s)) * kKeys;
+            const int bad = ct.facts[j % kFactsRing].bad;
+            const int zlo = key0 + kKeys > sg.prefix ? max(0, sg.prefix - key0) : kKeys;
+            uint8_t* vd = skv + st * Sm::kStageB + Sm::kTileB;
+            if (zlo < kKeys || bad) {
+              for (int idx = lane; idx < kKeys * Sm::kHalves * 8; idx += 32) {
+                const int row = idx / (Sm::kHalves * 8);
+                const int rem = idx - row * (Sm::kHalves * 8);
+                const int h = rem >> 3, c = rem & 7;
+                if (row >= zlo || ((bad >> (row >> 6)) & 1))
+                  *reinterpret_cast<uint4*>(vd + h * Sm::kHalfB + row * 128 + c * 16) =
+                      make_uint4(0, 0, 0, 0);
+              }
+              fence_async_smem();
+              __syncwarp();
+            }
+            v_addr = smem_u32(vd);
+          }
+        }
+        const int x = s & 1;
+        if (!mbar_wait(&ct.p_full[x], (cbase[x] + (s >> 1)) & 1, p.flags)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk) {
+            const uint64_t bd = sdesc(v_addr + kk * 2048, Sm::kHalfB, 1024);
+            mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, bd, id_o,
+                   (s >= 2 || kk > 0) ? 1u : 0u);
+          }
+          tc_commit(&ct.o_bar[x]);
+          if (last_of(s)) tc_commit(quant(kFmt) ? &ct.vc_free : &ct.v_empty[j % kStages]);
+        }
+        __syncwarp();
+        return true;
+      };
+      if (ok) ok = issue_s(0);
+      if (ok && nsteps > 1) ok = issue_s(1);
+      for (int s = 0; s < nsteps && ok; ++s) {
+        if (!(ok = issue_pv(s))) break;
+        if (s + 2 < nsteps) ok = issue_s(s + 2);
+      }
+      if (!ok) ct.abort = 1;
+    } else if (n > 0 && warp < 8) {
+      // ----------------------------------------------------------- softmax
+      const int x = warp >> 2;   // slot
+      const int wq = warp & 3;   // TMEM lane quadrant of this warp
+      const int r = wq * 32 + lane;  // row of the tile = TMEM lane
+      const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+      const uint32_t colS = col_s(x), colO = col_o(x);
+      const int b = sg.b0 + (pairs ? x * TQ : 0) + r / G;
+      const bool row_ok = b < sg.b1;
+      float m_ref = -INFINITY, l = 0.f;
+      const int mine = x ? steps_x[1] : steps_x[0];
+      const uint32_t c0 = x ? cbase[1] : cbase[0];
+      for (int q = 0; q < mine; ++q) {
+        const int i = pairs ? q : 2 * q + x;  // local key tile
+        const uint32_t j = jbase + i;
+        if (!mbar_wait(&ct.s_full[x], (c0 + q) & 1, p.flags) ||
+            !mbar_wait(&ct.facts_full[j % kFactsRing], (j / kFactsRing) & 1, p.flags)) {
+          ok = false;
+          break;
+        }
+        const TileFacts tf = ct.facts[j % kFactsRing];
+        tc_fence_after();
+        const int32_t key0 = (sg.tile0 + i) * kKeys;
+        const float mul0 = quant(kFmt) ? p.scale_log2 * tf.ks[0] : p.scale_log2;
+        const float mul1 = quant(kFmt) ? p.scale_log2 * tf.ks[1] : p.scale_log2;
+        // Quantised pools: the V scale of a 64-key block rides on P as an
+        // exponent, P = 2^(s - m + log2 vs), and m bounds s + log2 vs, so that
+        // the f16 P keeps its 11 bits whatever the scales are; the row sum takes
+        // P / vs.  (m is a reference only: l and o carry the same 2^-m.)  l is
+        // held 2^-60 smaller, so that it stays in range for every scale.
+        float lv0 = 0.f, lv1 = 0.f, iv0 = 1.f, iv1 = 1.f;
+        if constexpr (quant(kFmt)) {
+          const float v0 = fmaxf(tf.vs[0], kTiny), v1 = fmaxf(tf.vs[1], kTiny);
+          lv0 = log2f(v0), iv0 = kSumUnit / v0;
+          lv1 = log2f(v1), iv1 = kSumUnit / v1;
+        }
+        // A block is live whole or not at all: pages, and with them the prefix,
+        // end on 64 keys.
+        const bool on0 = !(tf.bad & 1);
+        const bool on1 = !(tf.bad & 2) && key0 + 64 < sg.prefix;
+        // Max of a block: of the raw scores for positive multipliers (max(s) * mul
+        // = max(s * mul)), else of the products.
+        auto block_max = [&](const float* sv, float mul) -> float {
+          float m0 = -INFINITY, m1 = -INFINITY;
+          if (mul > 0.f) {
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+              m0 = fmax3(m0, sv[e], sv[e + 1]);
+              m1 = fmax3(m1, sv[e + 2], sv[e + 3]);
+            }
+            return fmaxf(m0, m1) * mul;
+          }
+#pragma unroll
+          for (int e = 0; e < 64; ++e) m0 = fmaxf(m0, sv[e] * mul);
+          return m0;
+        };
+        // The reference rises lazily, when a row's max has grown by 2^8 (P <= 2^8
+        // in bf16 and in f16).  S of this step done implies the slot's earlier
+        // products are, so O may be rescaled; this step's PV waits for its P.
+        float alpha = 1.f;
+        auto set_max = [&](float mt) -> float {
+          const bool need = mt > m_ref + 8.f;
+          const float m_new = need ? mt : m_ref;
+          if (q >= 1 && need) alpha = fast_exp2(m_ref - m_new);
+          m_ref = m_new;
+          return m_ref == -INFINITY ? 0.f : m_ref;
+        };
+        float mt = -INFINITY;
+#pragma unroll
+        for (int cb = 0; cb < kKeys; cb += 64) {
+          float sv[64];
+          tmem_ld32(tmem + lane_base + colS + cb, sv);
+          tmem_ld32(tmem + lane_base + colS + cb + 32, sv + 32);
+          tmem_wait_ld();
+          if (cb < 64 ? on0 : on1)
+            mt = fmaxf(mt, block_max(sv, cb < 64 ? mul0 : mul1) + (cb < 64 ? lv0 : lv1));
+        }
+        const float m_use = set_max(mt);
+        float rs = 0.f;
+#pragma unroll
+        for (int cb = 0; cb < kKeys; cb += 64) {
+          float sv[64];
+          tmem_ld32(tmem + lane_base + colS + cb, sv);
+          tmem_ld32(tmem + lane_base + colS + cb + 32, sv + 32);
+          tmem_wait_ld();
+          uint32_t pk[32];
+          if (cb < 64 ? on0 : on1) {
+            const float mul = cb < 64 ? mul0 : mul1, off = (cb < 64 ? lv0 : lv1) - m_use;
+            float2 racc = make_float2(0.f, 0.f);
+            const float2 mul_2 = make_float2(mul, mul), off_2 = make_float2(off, off);
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+              const float2 t = fma2(make_float2(sv[e], sv[e + 1]), mul_2, off_2);
+              const float2 pp = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+              racc = add2(racc, pp);
+              pk[e / 2] = quant(kFmt) ? pack_f16(pp.x, pp.y) : pack_bf16(pp.x, pp.y);
+            }
+            rs += (racc.x + racc.y) * (cb < 64 ? iv0 : iv1);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) pk[e] = 0u;
+          }
+          // P column c/2 lies in an S column already read
+          tmem_st16(tmem + lane_base + colS + cb / 2, pk);
+          tmem_st16(tmem + lane_base + colS + cb / 2 + 16, pk + 16);
+        }
+        if (__any_sync(0xffffffffu, alpha != 1.f)) rescale_o<D>(tmem + lane_base + colO, alpha);
+        l = l * alpha + rs;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ct.p_full[x]);
+      }
+      // --------------------------------------------------------- partials
+      // Rows of slot x: float4 vectors [D/4][rows of the slot], so that a warp's
+      // lanes write consecutive 16 bytes; (m, l) beside them.  For quantised
+      // pools o takes l's unit, and m makes up for it.
+      constexpr float kUnit = quant(kFmt) ? kSumUnit : 1.f;
+      const int nr0 = min(sg.rows, kRows);  // rows of slot 0's Q tile
+      const int nr = pairs ? (x ? sg.rows - kRows : kRows) : sg.rows;
+      const bool out_ok = row_ok && r < nr;
+      if (ok && mine > 0 &&
+          !mbar_wait(&ct.o_bar[x], (c0 + mine - 1) & 1, p.flags))
+        ok = false;
+      if (ok) {
+        tc_fence_after();
+        const int64_t row0 = (int64_t)sg.row_base + (x ? nr0 : 0);
+        if (mine > 0) {
+          float4* dst = reinterpret_cast<float4*>(sp.pre_o) + row0 * (D / 4) + r;
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(tmem + lane_base + colO + c, o);
+            tmem_wait_ld();
+            if (out_ok) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                dst[(int64_t)((c + e) / 4) * nr] = make_float4(o[e] * kUnit, o[e + 1] * kUnit,
+                                                               o[e + 2] * kUnit, o[e + 3] * kUnit);
+            }
+          }
+        }
+        // (no step or no live key: l = 0; NaN passes)
+        if (out_ok) sp.pre_ml[row0 + r] = make_float2(m_ref + (quant(kFmt) ? 60.f : 0.f), l);
+      } else {
+        ct.abort = 1;
+      }
+    }
+
+    // ------------------------------------------------------ end of a segment
+    jbase += n;
+    cbase[0] += steps_x[0];
+    cbase[1] += steps_x[1];
+    if (n > 0) ++nseg;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) {
+      // the next item, if the range reaches into it
+      const int w = pair_tiles(cur.w, cur.pair);
+      const int64_t next_x = cur.item_x + (int64_t)cur.w.tiles * w;
+      more = next_x < x_end;
+      if (more) cur = locate(p, next_x, lane);
+      if (lane == 0) ct.more = more ? 1 : 0;
+    }
+  }
+
+  // ------------------------------------------------------------- teardown
+  if (warp == kMmaWarp) {
+    if (lane == 0) tc_commit(&ct.done_bar);
+    __syncwarp();
+    mbar_wait(&ct.done_bar, 0, p.flags);
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  // (A producer whose wait gave up issued its last load before that wait, whose
+  // whole limit the load had to land.)
+}
+
+// ------------------------------------------------------------------- merge
+// One warp per (sequence, kv head): adds up the prefix partials of its G rows
+// and the partials of the sequence's own tokens.  Launched as a programmatic
+// dependent of the decode kernel, whose completion (and memory) it awaits.
+template <int D, int G>
+__global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams sp) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const DecodeParams& p = sp.d;
+  const int lane = threadIdx.x & 31;
+  const int u = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (u >= p.batch * p.num_kv_heads) return;
+  const int b = u / p.num_kv_heads;
+  const int g = u - b * p.num_kv_heads;
+  const int32_t cap = p.max_pages * p.page_size;
+  const int32_t len = max(0, min(__ldg(p.seq_lens + b), cap));
+  const int32_t shared = shared_tokens(p.cu_groups, p.prefix_lens, p.num_groups, p.batch, b,
+                                       len, p.page_size, p.max_pages);
+  constexpr int kV = G * D / 128;  // float4 vectors of the unit's output per lane
+  static_assert(G * D % 128 == 0 || G * D == 64, "");
+  constexpr int kN = kV > 0 ? kV : 1;
+  // vector i of this lane: row v % G, dims 4 * (v / G) of v = lane + 32 i
+  float4 acc[kN];
+  float m[kN], l[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+  }
+  const bool on = lane * 4 < G * D;
+  auto add = [&](int i, float2 ml, float4 o) {
+    if (ml.y == 0.f) return;  // a part without keys: o is not written
+    const float mn = fmaxf(m[i], ml.x);
+    const float a = m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - mn);
+    const float c = fast_exp2(ml.x - mn);
+    acc[i].x = acc[i].x * a + o.x * c;
+    acc[i].y = acc[i].y * a + o.y * c;
+    acc[i].z = acc[i].z * a + o.z * c;
+    acc[i].w = acc[i].w * a + o.w * c;
+    l[i] = l[i] * a + ml.y * c;
+    m[i] = mn;
+  };
+  if (on && shared > 0 && len > 0) {
+    const int4 info = sp.pre_info[u];  // first row, segments, first sequence, rows
+    const int rows = info.w;
+    const bool pairs = rows > kRows;
+    const int nr0 = min(rows, kRows);
+    // (a prefix CTA that gave up may have left its word unwritten)
+    const bool sane = info.x >= 0 && info.y > 0 && info.y <= kMaxSegments && b >= info.z &&
+                      (b - info.z) * G < rows && rows <= kPairRows &&
+                      info.x + (info.y - 1) * (int64_t)kPairRows + (pairs ? rows : 2 * rows) <=
+                          sp.pre_rows;
+    for (int s = 0; s < (sane ? info.y : 0); ++s) {
+      for (int x = 0; x < (pairs ? 1 : 2); ++x) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int v = lane + 32 * i;
+          int r = (b - info.z) * G + v % G;
+          int64_t row0 = (int64_t)info.x + (int64_t)s * kPairRows;
+          int nr = nr0;
+          if (pairs) {
+            if (r >= kRows) row0 += nr0, r -= kRows, nr = rows - kRows;
+          } else if (x) {
+            row0 += nr0;
+          }
+          const float2 ml = __ldcg(sp.pre_ml + row0 + r);
+          const float4 o = __ldcg(reinterpret_cast<const float4*>(sp.pre_o) + row0 * (D / 4) +
+                                  (int64_t)(v / G) * nr + r);
+          add(i, ml, o);
+        }
+      }
+    }
+  }
+  if (on && len > shared) {
+    const int2 info = p.unit_info[u];
+    const bool sane = info.x >= 0 && info.y > 0 && (int64_t)info.x + info.y <= sp.own_slots;
+    for (int s = 0; s < (sane ? info.y : 0); ++s) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const int v = lane + 32 * i;
+        const int64_t row = ((int64_t)info.x + s) * G + v % G;
+        const float2 ml = __ldcg(p.part_ml + row);
+        const float4 o =
+            __ldcg(reinterpret_cast<const float4*>(p.part_o) + row * (D / 4) + v / G);
+        add(i, ml, o);
+      }
+    }
+  }
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int v = lane + 32 * i;
+    const int64_t row = (int64_t)b * p.num_q_heads + g * G + v % G;
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+    const uint2 o = make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv),
+                               pack_bf16(acc[i].z * inv, acc[i].w * inv));
+    *reinterpret_cast<uint2*>(p.out + row * D + 4 * (v / G)) = o;
+    if (p.lse && v < G)
+      p.lse[row] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
+  }
+}
+
+template <int D>
+cudaError_t merge_for(const SharedParams& sp, cudaStream_t stream) {
+  const int64_t units = (int64_t)sp.d.batch * sp.d.num_kv_heads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((units + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  switch (sp.d.group) {
+    case 1: return cudaLaunchKernelEx(&cfg, shared_merge_kernel<D, 1>, sp);
+    case 2: return cudaLaunchKernelEx(&cfg, shared_merge_kernel<D, 2>, sp);
+    case 4: return cudaLaunchKernelEx(&cfg, shared_merge_kernel<D, 4>, sp);
+    default: return cudaLaunchKernelEx(&cfg, shared_merge_kernel<D, 8>, sp);
+  }
+}
+
+template <int D, int kFmt>
+cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                   const SharedParams& p, int num_ctas, cudaStream_t stream) {
+  const size_t smem = 1024 + Smem<D, kFmt>::kBytes + sizeof(Control);
+  // The shared-memory attribute belongs to the current device: set it once
+  // per device and instantiation.
+  constexpr int kMaxDevices = 64;
+  static bool attr[kMaxDevices] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!attr[dev]) {
+      e = cudaFuncSetAttribute(prefix_kernel<D, kFmt>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+      attr[dev] = true;
+    }
+  }
+  prefix_kernel<D, kFmt><<<num_ctas, Smem<D, kFmt>::kThreads, smem, stream>>>(tq, tk, tv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace sh
+
+cudaError_t shared_prefix_run(int head_dim, int fmt, const CUtensorMap& tq, const CUtensorMap& tk,
+                              const CUtensorMap& tv, const SharedParams& p, int num_ctas,
+                              cudaStream_t stream) {
+  const bool d128 = head_dim == 128;
+  switch (fmt) {
+    case PKV_KV_NVFP4:
+      return d128 ? sh::launch<128, PKV_KV_NVFP4>(tq, tk, tv, p, num_ctas, stream)
+                  : sh::launch<64, PKV_KV_NVFP4>(tq, tk, tv, p, num_ctas, stream);
+    case PKV_KV_INT8:
+      return d128 ? sh::launch<128, PKV_KV_INT8>(tq, tk, tv, p, num_ctas, stream)
+                  : sh::launch<64, PKV_KV_INT8>(tq, tk, tv, p, num_ctas, stream);
+    case PKV_KV_FP8_E4M3:
+      return d128 ? sh::launch<128, PKV_KV_FP8_E4M3>(tq, tk, tv, p, num_ctas, stream)
+                  : sh::launch<64, PKV_KV_FP8_E4M3>(tq, tk, tv, p, num_ctas, stream);
+    default:
+      return d128 ? sh::launch<128, PKV_KV_BF16>(tq, tk, tv, p, num_ctas, stream)
+                  : sh::launch<64, PKV_KV_BF16>(tq, tk, tv, p, num_ctas, stream);
+  }
+}
+
+cudaError_t shared_merge_run(int head_dim, const SharedParams& p, cudaStream_t stream) {
+  return head_dim == 128 ? sh::merge_for<128>(p, stream) : sh::merge_for<64>(p, stream);
+}
+
+}  // namespace pkv
