@@ -265,6 +265,14 @@ __device__ TilePos locate_tile(const DecodeParams& p, int64_t v, int lane) {
   return {p.batch, 0, 0, run_v, run_r};
 }
 
+// In a call with shared prefixes this kernel starts while the prefix kernel
+// ends (a programmatic dependent of it that reads none of its results).  One
+// CTA stays until that kernel is complete, so that whoever waits for this
+// grid, the merge, has waited for both.
+__device__ __forceinline__ void await_prefix(const DecodeParams& p) {
+  if (p.cu_groups && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Fused append: the producer warp writes sequence b's newest token (K and V
 // of kv head g, from k_new/v_new [B][Hkv][D]) into pool row (pid, g, slot):
 // the bytes paged_kv_append writes for it (bf16 bits, or the one-byte codes
@@ -400,7 +408,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   __syncthreads();
   n_tiles = s_misc[0];
-  if (n_tiles == 0) return;
+  if (n_tiles == 0) {
+    if (warp == kProducerWarp) await_prefix(p);
+    return;
+  }
 
   if (warp == kFlushWarp) {
     // ---------------------------------------------------------- flush warp
@@ -643,6 +654,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t lo = issued > kStages ? issued - kStages : 0;
     for (int64_t k = lo; k < issued; ++k)
       mbar_wait(&full[k % kStages], (uint32_t)((k / kStages) & 1), p.flags);
+    await_prefix(p);
     return;
   }
 
@@ -1290,6 +1302,19 @@ template <int D, int kFmt, int kStages, int kSnap>
 cudaError_t decode_launch(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p,
                           int num_ctas, cudaStream_t stream) {
   const size_t smem = decode_smem_bytes<D, kFmt, kStages, kSnap>(p.group);
+  if (p.cu_groups) {  // may start under the prefix kernel before it
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_kernel<D, kFmt, kStages, kSnap>, tk, tv, p);
+  }
   decode_kernel<D, kFmt, kStages, kSnap><<<num_ctas, kThreads, smem, stream>>>(tk, tv, p);
   return cudaGetLastError();
 }

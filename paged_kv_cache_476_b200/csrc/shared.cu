@@ -221,6 +221,10 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
   const int G = p.group;
   const int TQ = kRows / G;  // sequences per Q tile
 
+  // The decode kernel behind this one reads none of its results: its CTAs take
+  // the SMs as they come free.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   // ------------------------------------------------ this CTA's range (warp 0)
   int64_t T = 0, Ce = 1, x_end = 0;
   Cursor cur{};
@@ -715,104 +719,167 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
 }
 
 // ------------------------------------------------------------------- merge
-// One warp per (sequence, kv head): adds up the prefix partials of its G rows
-// and the partials of the sequence's own tokens.  Launched as a programmatic
-// dependent of the decode kernel, whose completion (and memory) it awaits.
+// One CTA per (sequence, kv head): adds up the prefix partials of its G rows
+// and the partials of the sequence's own tokens.  The (m, l) of all parts come
+// first, spread over the threads, and give every part its weight
+// 2^(m_i - M); the sum over the o_i then has no chain through it: the warps
+// take parts in turn, eight vectors in flight a lane, and add up in shared
+// memory.  Launched as a programmatic dependent of the decode kernel, whose
+// completion (and memory) it awaits.
+constexpr int kMergeThreads = 128;
+constexpr int kMergeWarps = kMergeThreads / 32;
+
 template <int D, int G>
-__global__ void __launch_bounds__(128) shared_merge_kernel(const SharedParams sp) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const SharedParams sp) {
+  constexpr int kChunk = 2048 / G;         // parts whose weights fit the shared array
+  constexpr int kVecs = G * D / 4;         // float4 vectors of the unit's output
+  constexpr int kN = (kVecs + 31) / 32;    // of a lane
+  constexpr int kInFlight = kN >= 8 ? 1 : 8 / kN;  // parts a lane loads together
+  __shared__ float s_w[kChunk * G];
+  __shared__ float s_red[2][kMergeWarps][G];
+  __shared__ float4 s_acc[kMergeWarps][kVecs];
   const DecodeParams& p = sp.d;
-  const int lane = threadIdx.x & 31;
-  const int u = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (u >= p.batch * p.num_kv_heads) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int u = blockIdx.x;
   const int b = u / p.num_kv_heads;
   const int g = u - b * p.num_kv_heads;
+  // (the arguments do not change under the kernels: read before the wait)
   const int32_t cap = p.max_pages * p.page_size;
   const int32_t len = max(0, min(__ldg(p.seq_lens + b), cap));
   const int32_t shared = shared_tokens(p.cu_groups, p.prefix_lens, p.num_groups, p.batch, b,
                                        len, p.page_size, p.max_pages);
-  constexpr int kV = G * D / 128;  // float4 vectors of the unit's output per lane
-  static_assert(G * D % 128 == 0 || G * D == 64, "");
-  constexpr int kN = kV > 0 ? kV : 1;
-  // vector i of this lane: row v % G, dims 4 * (v / G) of v = lane + 32 i
-  float4 acc[kN];
-  float m[kN], l[kN];
-#pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    m[i] = -INFINITY;
-    l[i] = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // Where the parts lie (a CTA that gave up may have left its word unwritten).
+  int n_pre = 0, n_own = 0, per = 1, rows = 0;  // parts; parts and rows of a segment
+  int64_t pre_row = 0, own_row = 0;
+  if (shared > 0) {
+    const int4 info = __ldcg(sp.pre_info + u);  // first row, segments, first sequence, rows
+    rows = info.w;
+    per = rows > kRows ? 1 : 2;
+    if (info.x >= 0 && info.y > 0 && info.y <= kMaxSegments && b >= info.z &&
+        (b - info.z) * G < rows && rows <= kPairRows &&
+        info.x + (info.y - 1) * (int64_t)kPairRows + per * rows <= sp.pre_rows) {
+      n_pre = info.y * per;
+      pre_row = info.x;
+      rows |= (b - info.z) * G << 16;  // low half: rows, high half: this unit's first row
+    }
   }
-  const bool on = lane * 4 < G * D;
-  auto add = [&](int i, float2 ml, float4 o) {
-    if (ml.y == 0.f) return;  // a part without keys: o is not written
-    const float mn = fmaxf(m[i], ml.x);
-    const float a = m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - mn);
-    const float c = fast_exp2(ml.x - mn);
-    acc[i].x = acc[i].x * a + o.x * c;
-    acc[i].y = acc[i].y * a + o.y * c;
-    acc[i].z = acc[i].z * a + o.z * c;
-    acc[i].w = acc[i].w * a + o.w * c;
-    l[i] = l[i] * a + ml.y * c;
-    m[i] = mn;
+  if (len > shared) {
+    const int2 info = __ldcg(p.unit_info + u);
+    if (info.x >= 0 && info.y > 0 && (int64_t)info.x + info.y <= sp.own_slots) {
+      n_own = info.y;
+      own_row = (int64_t)info.x * G;
+    }
+  }
+  const int r0 = rows >> 16;
+  rows &= 0xffff;
+  // Prefix part i: slot 0 or 1 of segment i / per.  The rows of a slot start
+  // at `first`, `nr` of them; this unit's row 0 is row `r` there.
+  struct Place {
+    int64_t first;
+    int nr, r;
   };
-  if (on && shared > 0 && len > 0) {
-    const int4 info = sp.pre_info[u];  // first row, segments, first sequence, rows
-    const int rows = info.w;
-    const bool pairs = rows > kRows;
-    const int nr0 = min(rows, kRows);
-    // (a prefix CTA that gave up may have left its word unwritten)
-    const bool sane = info.x >= 0 && info.y > 0 && info.y <= kMaxSegments && b >= info.z &&
-                      (b - info.z) * G < rows && rows <= kPairRows &&
-                      info.x + (info.y - 1) * (int64_t)kPairRows + (pairs ? rows : 2 * rows) <=
-                          sp.pre_rows;
-    for (int s = 0; s < (sane ? info.y : 0); ++s) {
-      for (int x = 0; x < (pairs ? 1 : 2); ++x) {
+  auto place = [&](int i) -> Place {
+    if (per == 1) {  // two Q tiles: the unit's rows lie in one of them
+      const int64_t base = pre_row + (int64_t)i * kPairRows;
+      return r0 < kRows ? Place{base, kRows, r0} : Place{base + kRows, rows - kRows, r0 - kRows};
+    }
+    return {pre_row + (int64_t)(i >> 1) * kPairRows + (i & 1) * rows, rows, r0};
+  };
+  auto ml_of = [&](int i, int row) -> float2 {
+    if (i < n_pre) {
+      const Place pl = place(i);
+      return __ldcg(sp.pre_ml + pl.first + pl.r + row);
+    }
+    return __ldcg(p.part_ml + own_row + (int64_t)(i - n_pre) * G + row);
+  };
+
+  // The largest reference of each row: thread t looks at row t % G.
+  const int n = n_pre + n_own;
+  const int my_row = threadIdx.x % G, my_part = threadIdx.x / G;
+  constexpr int kStep = kMergeThreads / G;
+  float M = -INFINITY;
+  for (int i = my_part; i < n; i += kStep) {
+    const float2 ml = ml_of(i, my_row);
+    if (ml.y != 0.f) M = fmaxf(M, ml.x);  // l = 0: a part without keys, its o is not written
+  }
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const int v = lane + 32 * i;
-          int r = (b - info.z) * G + v % G;
-          int64_t row0 = (int64_t)info.x + (int64_t)s * kPairRows;
-          int nr = nr0;
-          if (pairs) {
-            if (r >= kRows) row0 += nr0, r -= kRows, nr = rows - kRows;
-          } else if (x) {
-            row0 += nr0;
-          }
-          const float2 ml = __ldcg(sp.pre_ml + row0 + r);
-          const float4 o = __ldcg(reinterpret_cast<const float4*>(sp.pre_o) + row0 * (D / 4) +
-                                  (int64_t)(v / G) * nr + r);
-          add(i, ml, o);
+  for (int o = G; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane < G) s_red[0][warp][lane] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, s_red[0][w][my_row]);
+
+  float4 acc[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float L = 0.f;
+  for (int c0 = 0; c0 < n; c0 += kChunk) {
+    const int cn = min(n - c0, kChunk);
+    if (c0 > 0) __syncthreads();  // the last chunk's weights have been used
+    for (int i = my_part; i < cn; i += kStep) {
+      const float2 ml = ml_of(c0 + i, my_row);
+      const float w = ml.y != 0.f ? fast_exp2(ml.x - M) : 0.f;
+      s_w[i * G + my_row] = w;
+      L += w * ml.y;
+    }
+    __syncthreads();
+    for (int i0 = warp * kInFlight; i0 < cn; i0 += kMergeWarps * kInFlight) {
+      float4 o[kInFlight][kN];
+      float w[kInFlight][kN];
+#pragma unroll
+      for (int k = 0; k < kInFlight; ++k) {
+        const int i = c0 + i0 + k;
+        const bool pre = i < n_pre;
+        const Place pl = pre ? place(i) : Place{own_row + (int64_t)(i - n_pre) * G, 0, 0};
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+          const int v = lane + 32 * j;  // row v % G, dims 4 * (v / G)
+          w[k][j] = i0 + k < cn && (kVecs >= 32 || v < kVecs) ? s_w[(i0 + k) * G + v % G] : 0.f;
+          o[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (w[k][j] != 0.f)
+            o[k][j] = pre ? __ldcg(reinterpret_cast<const float4*>(sp.pre_o) + pl.first * (D / 4) +
+                                   (int64_t)(v / G) * pl.nr + pl.r + v % G)
+                          : __ldcg(reinterpret_cast<const float4*>(p.part_o) +
+                                   (pl.first + v % G) * (D / 4) + v / G);
         }
       }
+#pragma unroll
+      for (int k = 0; k < kInFlight; ++k)
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+          acc[j].x += w[k][j] * o[k][j].x;
+          acc[j].y += w[k][j] * o[k][j].y;
+          acc[j].z += w[k][j] * o[k][j].z;
+          acc[j].w += w[k][j] * o[k][j].w;
+        }
     }
   }
-  if (on && len > shared) {
-    const int2 info = p.unit_info[u];
-    const bool sane = info.x >= 0 && info.y > 0 && (int64_t)info.x + info.y <= sp.own_slots;
-    for (int s = 0; s < (sane ? info.y : 0); ++s) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const int v = lane + 32 * i;
-        const int64_t row = ((int64_t)info.x + s) * G + v % G;
-        const float2 ml = __ldcg(p.part_ml + row);
-        const float4 o =
-            __ldcg(reinterpret_cast<const float4*>(p.part_o) + row * (D / 4) + v / G);
-        add(i, ml, o);
-      }
+  for (int o = G; o < 32; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (lane < G) s_red[1][warp][lane] = L;
+#pragma unroll
+  for (int j = 0; j < kN; ++j)
+    if (kVecs >= 32 || lane < kVecs) s_acc[warp][lane + 32 * j] = acc[j];
+  __syncthreads();
+  for (int v = threadIdx.x; v < kVecs; v += kMergeThreads) {
+    const int row = v % G;
+    float4 a = s_acc[0][v];
+    float l = s_red[1][0][row];
+#pragma unroll
+    for (int w = 1; w < kMergeWarps; ++w) {
+      const float4 x = s_acc[w][v];
+      a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+      l += s_red[1][w][row];
     }
-  }
-  if (!on) return;
-#pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    const int v = lane + 32 * i;
-    const int64_t row = (int64_t)b * p.num_q_heads + g * G + v % G;
-    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-    const uint2 o = make_uint2(pack_bf16(acc[i].x * inv, acc[i].y * inv),
-                               pack_bf16(acc[i].z * inv, acc[i].w * inv));
-    *reinterpret_cast<uint2*>(p.out + row * D + 4 * (v / G)) = o;
+    const int64_t orow = (int64_t)b * p.num_q_heads + g * G + row;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2*>(p.out + orow * D + 4 * (v / G)) =
+        make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+    // (M belongs to row threadIdx.x % G, which is v % G)
     if (p.lse && v < G)
-      p.lse[row] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
+      p.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
   }
 }
 
@@ -820,8 +887,8 @@ template <int D>
 cudaError_t merge_for(const SharedParams& sp, cudaStream_t stream) {
   const int64_t units = (int64_t)sp.d.batch * sp.d.num_kv_heads;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((units + 3) / 4));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((unsigned)units);
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
