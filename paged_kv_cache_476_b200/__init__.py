@@ -226,9 +226,13 @@ def _dev(name: str, t: torch.Tensor, dtype=None, ndim=None):
     return t
 
 
+# The raw handle of a device's current stream (a Stream object takes 3 us to make).
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return ctypes.c_void_p(_current_raw_stream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -239,26 +243,29 @@ def _rows(name: str, t: torch.Tensor) -> int:
     if t.dtype is not torch.bfloat16 or t.dim() != 3:
         raise ValueError(f"{name} must be a bfloat16 tensor [tokens, heads, head_dim]")
     T, H, D = t.shape
-    s = t.stride()
-    if D > 1 and s[2] != 1 or H > 1 and s[1] != D:
+    s0, s1, s2 = t.stride()
+    if D > 1 and s2 != 1 or H > 1 and s1 != D:
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return s[0] if T > 1 else H * D
+    return s0 if T > 1 else H * D
 
 
 def _same_device(device: torch.device, **tensors):
+    index = device.index
     for name, t in tensors.items():
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"{name} is on {t.device}, not {device}")
 
 
-def _result(name: str, t: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
-    """A result tensor: the caller's, checked, or a new one."""
+def _result(name: str, t: Optional[torch.Tensor], like: torch.Tensor, shape,
+            dtype=None) -> torch.Tensor:
+    """A result tensor of ``like``'s device and (by default) dtype: the caller's,
+    checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _dev(name, t, dtype)
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+    _dev(name, t, dtype or like.dtype)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    _same_device(device, **{name: t})
+    _same_device(like.device, **{name: t})
     return t
 
 
@@ -266,7 +273,7 @@ def _on(device: torch.device, stream, call):
     """``call(raw stream)`` with ``device`` and ``stream`` current, so that what
     the call allocates belongs to the stream that uses it."""
     if stream is None and device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
+        return call(_current_raw_stream(device.index))
     if stream is not None and not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device)
     if stream is not None and stream.device != device:
@@ -333,6 +340,7 @@ class PagedKVCache:
                            self.num_pages, self.page_size, self.num_kv_heads, self.head_dim,
                            _KV_CODES[kv_dtype],
                            None if error_flags is None else error_flags.data_ptr())
+        self._ref = ctypes.byref(self._c)
 
     @property
     def c_struct(self) -> PkvCache:
@@ -398,6 +406,7 @@ class Rope:
                           None if q_norm_weight is None else q_norm_weight.data_ptr(),
                           None if k_norm_weight is None else k_norm_weight.data_ptr(),
                           self.norm_eps)
+        self._ref = ctypes.byref(self._c)
 
     @property
     def c_struct(self) -> PkvRope:
@@ -406,8 +415,8 @@ class Rope:
     def _check(self, head_dim: int, device: torch.device):
         if self.device is not None and self.device != device:
             raise ValueError(f"the rotation's tensors are on {self.device}, not {device}")
-        for name in ("q_norm_weight", "k_norm_weight"):
-            w = getattr(self, name)
+        for name, w in (("q_norm_weight", self.q_norm_weight),
+                        ("k_norm_weight", self.k_norm_weight)):
             if w is not None and w.shape[0] != head_dim:
                 raise ValueError(f"{name} must have head_dim = {head_dim} entries")
 
@@ -422,14 +431,19 @@ def pkv_qk_norm_rope(rope: Rope, q, k, positions=None, q_out=None, k_out=None, e
     Returns ``(q_out, k_out)``; rows of tokens with a position outside the
     table keep what they held and raise ``PKV_FLAG_BAD_LENGTH``.
     """
-    if q is None and k is None:
+    x = k if q is None else q
+    if x is None:
         raise ValueError("q or k must be given")
-    T, _, D = (k if q is None else q).shape
-    device = (k if q is None else q).device
-    qs = 0 if q is None else _rows("q", q)
-    ks = 0 if k is None else _rows("k", k)
-    if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != D):
-        raise ValueError("q and k must have the same tokens and head_dim")
+    qs = ks = Hq = Hkv = 0
+    if k is not None:
+        ks = _rows("k", k)
+        T, Hkv, D = k.shape
+    if q is not None:
+        qs = _rows("q", q)
+        T, Hq, D = q.shape
+        if k is not None and (k.shape[0] != T or k.shape[2] != D):
+            raise ValueError("q and k must have the same tokens and head_dim")
+    device = x.device
     if rope.cos_sin is not None:
         _dev("positions", positions, torch.int32, 1)
         if positions.shape[0] != T:
@@ -440,12 +454,11 @@ def pkv_qk_norm_rope(rope: Rope, q, k, positions=None, q_out=None, k_out=None, e
     _same_device(device, k=k, positions=positions, error_flags=error_flags)
 
     def call(s):
-        qo = None if q is None else _result("q_out", q_out, q.shape, torch.bfloat16, device)
-        ko = None if k is None else _result("k_out", k_out, k.shape, torch.bfloat16, device)
+        qo = None if q is None else _result("q_out", q_out, q, q.shape)
+        ko = None if k is None else _result("k_out", k_out, k, k.shape)
         _check("pkv_qk_norm_rope", _lib.pkv_qk_norm_rope(
-            ctypes.byref(rope.c_struct), None if q is None else q.data_ptr(), qs,
-            0 if q is None else q.shape[1], None if k is None else k.data_ptr(), ks,
-            0 if k is None else k.shape[1], D,
+            rope._ref, None if q is None else q.data_ptr(), qs, Hq,
+            None if k is None else k.data_ptr(), ks, Hkv, D,
             None if positions is None else positions.data_ptr(), T,
             None if q is None else qo.data_ptr(), None if k is None else ko.data_ptr(),
             None if error_flags is None else error_flags.data_ptr(), s))
@@ -472,17 +485,21 @@ def paged_kv_append_rope(cache: PagedKVCache, rope: Rope, page_table, seq_lens_b
     _dev("cu_new_tokens", cu_new_tokens, torch.int32, 1)
     ks, vs = _rows("k_new", k_new), _rows("v_new", v_new)
     device = cache.k_pool.device
-    T = k_new.shape[0] if total_new_tokens is None else int(total_new_tokens)
-    B, D = seq_lens_before.shape[0], cache.head_dim
-    if k_new.shape != v_new.shape or tuple(k_new.shape[1:]) != (cache.num_kv_heads, D):
+    rows, Hkv, D = shape = k_new.shape
+    T = rows if total_new_tokens is None else int(total_new_tokens)
+    B, = seq_lens_before.shape
+    if v_new.shape != shape or Hkv != cache.num_kv_heads or D != cache.head_dim:
         raise ValueError("k_new and v_new must be [tokens, num_kv_heads, head_dim]")
-    if page_table.shape[0] != B or cu_new_tokens.shape[0] != B + 1:
+    table_rows, max_pages = page_table.shape
+    if table_rows != B or cu_new_tokens.shape[0] != B + 1:
         raise ValueError("page_table and cu_new_tokens must match seq_lens_before")
-    if T > k_new.shape[0]:
+    if T > rows:
         raise ValueError("total_new_tokens exceeds the tokens given")
+    qs = Hq = 0
     if q is not None:
         qs = _rows("q", q)
-        if q.shape[0] < T or q.shape[2] != D:
+        q_rows, Hq, q_dim = q.shape
+        if q_rows < T or q_dim != D:
             raise ValueError("q must be [tokens, q heads, head_dim]")
     if positions is not None:
         _dev("positions", positions, torch.int32, 1)
@@ -493,13 +510,11 @@ def paged_kv_append_rope(cache: PagedKVCache, rope: Rope, page_table, seq_lens_b
                  cu_new_tokens=cu_new_tokens, k_new=k_new, v_new=v_new, q=q, positions=positions)
 
     def call(s):
-        out = None if q is None else _result("q_out", q_out, q.shape, torch.bfloat16, device)
+        out = None if q is None else _result("q_out", q_out, q, q.shape)
         _check("paged_kv_append_rope", _lib.paged_kv_append_rope(
-            ctypes.byref(cache.c_struct), ctypes.byref(rope.c_struct), page_table.data_ptr(),
-            page_table.shape[1], seq_lens_before.data_ptr(), cu_new_tokens.data_ptr(), B, T,
-            k_new.data_ptr(), ks, v_new.data_ptr(), vs, None if q is None else q.data_ptr(),
-            0 if q is None else qs, 0 if q is None else q.shape[1],
-            None if q is None else out.data_ptr(),
+            cache._ref, rope._ref, page_table.data_ptr(), max_pages, seq_lens_before.data_ptr(), cu_new_tokens.data_ptr(), B, T,
+            k_new.data_ptr(), ks, v_new.data_ptr(), vs, None if q is None else q.data_ptr(), qs,
+            Hq, None if q is None else out.data_ptr(),
             None if positions is None else positions.data_ptr(), s))
         return out
 
@@ -626,11 +641,12 @@ def paged_decode_attention_shared(cache: PagedKVCache, q, page_table, seq_lens, 
                     ("prefix_lens", prefix_lens)):
         _dev(name, t, torch.int32, 1)
     B, Hq, D = q.shape
-    groups = prefix_lens.shape[0]
+    groups, = prefix_lens.shape
+    table_rows, max_pages = page_table.shape
     device = cache.k_pool.device
     if D != cache.head_dim:
         raise ValueError(f"q must have head_dim = {cache.head_dim}")
-    if page_table.shape[0] != B or seq_lens.shape[0] != B:
+    if table_rows != B or seq_lens.shape[0] != B:
         raise ValueError("page_table and seq_lens must match q")
     if cu_groups.shape[0] != groups + 1:
         raise ValueError("cu_groups must have one entry more than prefix_lens")
@@ -643,16 +659,16 @@ def paged_decode_attention_shared(cache: PagedKVCache, q, page_table, seq_lens, 
         softmax_scale = 1.0 / math.sqrt(D)
 
     def call(s):
-        o = _result("out", out, (B, Hq, D), torch.bfloat16, device)
+        o = _result("out", out, q, (B, Hq, D))
         l = None
         if lse is not None or want_lse:
-            l = _result("lse", lse, (B, Hq), torch.float32, device)
+            l = _result("lse", lse, q, (B, Hq), torch.float32)
         w = workspace
         if w is None:
             w = decode_shared_workspace(cache, B, Hq, int(max_seq_len), groups)
         _check("paged_decode_attention_shared", _lib.paged_decode_attention_shared(
-            ctypes.byref(cache.c_struct), q.data_ptr(), Hq, Hq // cache.num_kv_heads,
-            page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), B, int(max_seq_len),
+            cache._ref, q.data_ptr(), Hq, Hq // cache.num_kv_heads,
+            page_table.data_ptr(), max_pages, seq_lens.data_ptr(), B, int(max_seq_len),
             cu_groups.data_ptr(), prefix_lens.data_ptr(), groups, float(softmax_scale),
             o.data_ptr(), None if l is None else l.data_ptr(), w.data_ptr(), w.nbytes, s))
         return o, l
