@@ -23,15 +23,17 @@
 //    accumulators (slot 0 the even ones, slot 1 the odd), so that one slot's
 //    softmax runs under the other's products there too; both slots leave
 //    partials.
-//  * Roles as in the prefill kernel: warps 0-3 and 4-7 softmax of slot 0 and 1,
-//    one TMEM lane a row; warp 8 loads (Q by a 3-D map, K and V tiles page by
-//    page into two-slot rings); warp 9 issues the MMAs, S = Q K^T and
-//    O += P V with P from TMEM; two warps convert quantised tiles.  Step i
-//    belongs to slot i & 1 whatever the mode: step i's PV, then step i + 2's S.
-//  * The segments of a CTA run one after the other between barriers; rings and
-//    phases carry on across them.
-//  * Quantised K and V: codes convert exactly to 16 bits; the K scales multiply
-//    the scores of their 64-key block, the V scales ride on P.
+//  * Roles: warps 0-3 and 4-7 softmax of slot 0 and 1, one TMEM lane a row;
+//    warp 8 loads (Q by a 3-D map, K and V tiles page by page into rings);
+//    warp 9 issues the MMAs, S = Q K^T and O += P V with P from TMEM; warp 10
+//    walks the work list and hands out segments.  Step i of a segment belongs
+//    to slot i & 1 whatever the mode: step i's PV, then step i + 2's S.
+//  * Each role walks the segments on its own; only barriers on the data tie
+//    them, so loads (and conversions) run ahead across segments.
+//  * Quantised K and V: four more warps convert codes exactly to f16, and Q's
+//    rows (times powers of two) with them; the K scales multiply the scores of
+//    their 64-key block, the V scales ride on P.  The softmax warps take the
+//    registers that the other warps give up.
 //  * Every wait is bounded; a timeout ends the CTA with the error flag set.
 #include <mutex>
 
@@ -45,20 +47,27 @@ namespace sh {
 
 using namespace pf;
 
-constexpr int kStages = 2;     // K/V ring depth
+// Warps: 0-3 and 4-7 softmax of slot 0 and 1, then the roles below; quantised
+// pools add a warpgroup of converters.
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
-constexpr int kConvWarp0 = 10;
-constexpr int kConvWarps = 2;
+constexpr int kSchedWarp = 10;  // warp 11 has no role
+constexpr int kConvWarp0 = 12;
+constexpr int kConvWarps = 4;
 constexpr int kConvThreads = kConvWarps * 32;
-// A facts slot is refilled when tile j - 2 has left the K ring.  With one Q
-// tile the softmax of tile j - 4 may still run then (the converters are ahead
-// of the products), so eight slots.
-constexpr int kFactsRing = 8;
+constexpr int kSegRing = 2;  // segment descriptors ahead
+// A facts slot is refilled when the K ring has let go of a tile (at most
+// kMaxStages tiles back); the softmax may be three tiles behind that.
+constexpr int kMaxStages = 5;
+constexpr int kFactsRing = 16;
 constexpr int kPairRows = 2 * kRows;
 constexpr int kMaxSegments = 1 << 16;     // more than any GPU has SMs
 constexpr float kTiny = 1.17549435e-38f;       // smallest normal fp32
 constexpr float kSumUnit = 1.f / (1ull << 60);  // unit of l for quantised pools
+
+// Registers of the softmax and of the other warps for quantised pools: 256 x
+// 176 + 256 x 80 = 512 x 128, what the block is launched with.
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80, kLaunchRegs = 128;
 
 struct TileFacts {
   int32_t bad;  // bit per 64-key block: rejected page
@@ -68,44 +77,76 @@ struct TileFacts {
 
 // One CTA's part of an item.
 struct Segment {
-  int32_t b0, b1;        // sequences of the item
-  int32_t b_table;       // sequence whose table row holds the prefix's pages
+  int32_t b0, b1;    // sequences of the item
+  int32_t b_table;   // sequence whose table row holds the prefix's pages
   int32_t head;
-  int32_t rows;          // (b1 - b0) * G
-  int32_t prefix;        // tokens
-  int32_t tile0, tile1;  // key tiles of the segment
-  int32_t row_base;      // first partial row of the segment
+  int32_t rows;      // (b1 - b0) * G
+  int32_t prefix;    // tokens
+  int32_t tile0, n;  // key tiles of the segment; n = 0: no more segments
+  int32_t row_base;  // first partial row of the segment
 };
+
+// Barriers and small state in front of the tiles.
+struct Control {
+  uint64_t seg_full[kSegRing], seg_empty[kSegRing];
+  uint64_t q_full, q_empty, qc_full;  // Q landed, free again, converted
+  uint64_t k_full[kMaxStages + 1], k_empty[kMaxStages + 1];
+  uint64_t v_full[kMaxStages + 1], v_empty[kMaxStages + 1];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t kc_full, kc_free, vc_full, vc_free;  // converted tiles
+  uint64_t facts_full[kFactsRing];
+  uint64_t done;
+  TileFacts facts[kFactsRing];
+  Segment seg[kSegRing];
+  uint32_t tmem;
+  // quantised pools: Q rows are 2^q_exp times f16, by segment parity and tile
+  int8_t q_exp[2][2][kRows];
+};
+
+constexpr int kSmemLimit = 227 * 1024;
+constexpr int kControlB = 2048;
+static_assert(sizeof(Control) <= kControlB, "");
 
 template <int D, int kFmt>
 struct Smem {
   static constexpr int kHalves = D / 64;        // 128-byte column boxes per bf16 row
   static constexpr int kQB = kRows * D * 2;     // one Q tile
-  static constexpr int kTileB = kKeys * D * 2;  // bf16 K (or V) tile
-  static constexpr int kHalfB = kKeys * 128;    // one 64-column half of a bf16 tile
+  static constexpr int kTileB = kKeys * D * 2;  // 16-bit K (or V) tile
+  static constexpr int kHalfB = kKeys * 128;    // one 64-column half of a 16-bit tile
   static constexpr int kCodeRowB = row_code_bytes(kFmt, D);
   static constexpr int kScaleRowB = row_scale_bytes(kFmt, D);
   static constexpr int kCodesB = kKeys * kCodeRowB;
   static constexpr int kTileQB = kCodesB + kKeys * kScaleRowB;
-  static constexpr int kStageB = quant(kFmt) ? 2 * kTileQB : 2 * kTileB;
+  static constexpr int kOperandB = quant(kFmt) ? kTileQB : kTileB;  // K (or V) of a stage
+  static constexpr int kStageB = 2 * kOperandB;
   static constexpr int kConvB = quant(kFmt) ? 2 * kTileB : 0;  // converted K, then V
-  static constexpr int kBytes = 2 * kQB + kStages * kStageB + kConvB;
-  static constexpr int kThreads = (quant(kFmt) ? kConvWarp0 + kConvWarps : kConvWarp0) * 32;
+  static constexpr int kRoom = kSmemLimit - 1024 - kControlB - 2 * kQB - kConvB;
+  static constexpr int kStages = kRoom / kStageB < kMaxStages ? kRoom / kStageB : kMaxStages;
+  // An item with one Q tile leaves the other's place free: with what is left of
+  // the room it makes one stage more (K there, V in the rest), which only the
+  // two-stage ring of bf16 at D = 128 has the need of.
+  static constexpr bool kExtra = !quant(kFmt) && kStages == 2 && kQB >= kOperandB &&
+                                 kRoom - kStages * kStageB >= kOperandB;
+  // (1024: the tiles' alignment)
+  static constexpr int kBytes = 1024 + kControlB + 2 * kQB + kStages * kStageB + kConvB +
+                                (kExtra ? kOperandB : 0);
+  static constexpr int kThreads = quant(kFmt) ? (kConvWarp0 + kConvWarps) * 32 : kConvWarp0 * 32;
+  static_assert(kStages >= 2, "");
 };
 
-// Barriers and small state behind the tiles.
-struct Control {
-  uint64_t q_full;
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_full[2], o_bar[2];
-  uint64_t done_bar;
-  uint64_t kc_full, kc_free, vc_full, vc_free;
-  uint64_t facts_full[kFactsRing];
-  TileFacts facts[kFactsRing];
-  Segment seg;
-  int32_t more;   // a segment is in `seg`
-  int32_t abort;  // a wait gave up
-  uint32_t tmem;
+// A role's place in the K/V ring: the slot of its next tile and the parity of
+// each slot's next fill.  Every role walks the same slots.
+struct Ring {
+  int slot = 0;
+  uint32_t parities = 0;
+  __device__ __forceinline__ void enter(int depth) {
+    if (slot >= depth) slot = 0;
+  }
+  __device__ __forceinline__ uint32_t parity() const { return (parities >> slot) & 1; }
+  __device__ __forceinline__ void advance(int depth) {
+    parities ^= 1u << slot;
+    if (++slot >= depth) slot = 0;
+  }
 };
 
 // ---------------------------------------------------------------- work list
@@ -180,10 +221,16 @@ __device__ Cursor locate(const DecodeParams& p, int64_t x, int lane) {
   return c;
 }
 
-// Steps of all items.  Warp-wide.
-__device__ int64_t total_steps(const DecodeParams& p, int lane) {
+// Steps of all items, and whether some group has two Q tiles.  Warp-wide.
+__device__ int64_t total_steps(const DecodeParams& p, int lane, bool* pairs) {
   int64_t t = 0;
-  for (int g = lane; g < p.num_groups; g += 32) t += group_work(p, g).steps;
+  bool two = false;
+  for (int g = lane; g < p.num_groups; g += 32) {
+    const GroupWork w = group_work(p, g);
+    t += w.steps;
+    two |= w.q_tiles > 1;
+  }
+  *pairs = __any_sync(0xffffffffu, two);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   return t * p.num_kv_heads;
@@ -201,6 +248,56 @@ __device__ int first_holder(const DecodeParams& p, const GroupWork& w, int lane)
   return -1;
 }
 
+// Row r of a bf16 Q tile (128-byte swizzled column boxes) to f16 in place, times
+// 2^e; returns e.
+template <int D>
+__device__ __forceinline__ int q_row_to_f16(uint32_t base, int r) {
+  float amax = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(bf16_chunk<D>(base, r, c)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+      amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+    }
+  }
+  int e = 0;
+  if (amax > 0.f && amax <= 3.4028235e38f) {
+    frexpf(amax, &e);                  // amax < 2^e
+    e = max(-114, min(100, 15 - e));   // amax * 2^e < 2^15
+  }
+  const float pre = ldexpf(1.f, e);
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint32_t at = bf16_chunk<D>(base, r, c);
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+      w[i] = pack_f16(f.x * pre, f.y * pre);
+    }
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3])
+                 : "memory");
+  }
+  return e;
+}
+
+template <int kRegs, bool kMore>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (kMore)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 template <int D, int kFmt>
 __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -211,10 +308,19 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* sq = smem;                            // Q tile A, then Q tile B
-  uint8_t* skv = smem + 2 * Sm::kQB;             // stage s: K at s*kStageB, V after it
-  uint8_t* sconv = skv + kStages * Sm::kStageB;  // quantised: 16-bit K, then V
-  Control& ct = *reinterpret_cast<Control*>(smem + Sm::kBytes);
+  Control& ct = *reinterpret_cast<Control*>(smem);
+  uint8_t* sq = smem + kControlB;                // Q tile A, then Q tile B
+  uint8_t* sconv = sq + 2 * Sm::kQB;             // quantised: 16-bit K, then V
+  uint8_t* skv = sconv + Sm::kConvB;             // stage s: K at s * kStageB, V after it
+  auto k_slot = [&](int st) -> uint8_t* {
+    if (Sm::kExtra && st == Sm::kStages) return sq + Sm::kQB;
+    return skv + st * Sm::kStageB;
+  };
+  auto v_slot = [&](int st) -> uint8_t* {
+    if (Sm::kExtra && st == Sm::kStages) return skv + Sm::kStages * Sm::kStageB;
+    return skv + st * Sm::kStageB + Sm::kOperandB;
+  };
+  auto ring_depth = [](bool pairs) { return Sm::kStages + (Sm::kExtra && !pairs ? 1 : 0); };
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -225,35 +331,16 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
   // the SMs as they come free.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ------------------------------------------------ this CTA's range (warp 0)
-  int64_t T = 0, Ce = 1, x_end = 0;
-  Cursor cur{};
-  bool more = false;  // warp 0: `cur` is a segment to run
-  if (warp == 0) {
-    T = total_steps(p, lane);
-    // two steps a CTA at least, so that every range holds a whole tile
-    Ce = min((int64_t)gridDim.x, T / 2);
-    if (Ce < 1) Ce = 1;
-    const int64_t c = blockIdx.x;
-    more = c < Ce && T > 0;
-    if (more) {
-      cur = locate(p, c * T / Ce, lane);
-      x_end = (c + 1) * T / Ce;
-    }
-    if (lane == 0) {
-      ct.more = more ? 1 : 0;
-      ct.abort = 0;
-    }
-    if (c == 0)
-      for (int g = lane; g < p.num_groups; g += 32) {
-        const int32_t b0 = __ldg(p.cu_groups + g), b1 = __ldg(p.cu_groups + g + 1);
-        if (b0 < 0 || b1 < b0 || b1 > p.batch || __ldg(p.prefix_lens + g) < 0)
-          flag_error(p.flags, PKV_FLAG_BAD_LENGTH);
-      }
-  }
   if (warp == 1 && lane == 0) {
+    for (int s = 0; s < kSegRing; ++s) {
+      mbar_init(&ct.seg_full[s], 1);
+      // producer, MMA, softmax warps, converters
+      mbar_init(&ct.seg_empty[s], 2 + 8 + (quant(kFmt) ? kConvWarps : 0));
+    }
     mbar_init(&ct.q_full, 1);
-    for (int s = 0; s < kStages; ++s) {
+    mbar_init(&ct.q_empty, 1);
+    mbar_init(&ct.qc_full, kConvWarps);
+    for (int s = 0; s < kMaxStages + 1; ++s) {
       mbar_init(&ct.k_full[s], 1);
       mbar_init(&ct.v_full[s], 1);
       // quantised: released by the converter warps
@@ -263,14 +350,14 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
     for (int x = 0; x < 2; ++x) {
       mbar_init(&ct.s_full[x], 1);
       mbar_init(&ct.p_full[x], 4);
-      mbar_init(&ct.o_bar[x], 1);
+      mbar_init(&ct.o_full[x], 1);
     }
-    mbar_init(&ct.done_bar, 1);
     mbar_init(&ct.kc_full, kConvWarps);
     mbar_init(&ct.kc_free, 1);
     mbar_init(&ct.vc_full, kConvWarps);
     mbar_init(&ct.vc_free, 1);
     for (int s = 0; s < kFactsRing; ++s) mbar_init(&ct.facts_full[s], 1);
+    mbar_init(&ct.done, 1);
     fence_barrier_init();
   }
   if (warp == kMmaWarp) tmem_alloc(&ct.tmem, kTmemCols);
@@ -278,283 +365,39 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ct.tmem;
+  // Segment number `k` (each warp that works on segments takes every one).
+  auto take_segment = [&](uint32_t k, Segment* sg) -> bool {
+    if (!mbar_wait(&ct.seg_full[k % kSegRing], (k / kSegRing) & 1, p.flags)) return false;
+    *sg = ct.seg[k % kSegRing];
+    return sg->n > 0;
+  };
 
-  // Carried across segments: key tiles and Q loads so far (every role counts
-  // the same), and the steps of each slot.
-  uint32_t jbase = 0, nseg = 0;
-  uint32_t cbase[2] = {0, 0};
-
-  while (true) {
-    // -------------------------------------------------- the next segment
-    const int b_table = more ? first_holder(p, cur.w, lane) : -1;
-    if (more && lane == 0) {
-      const int w = pair_tiles(cur.w, cur.pair);
-      Segment s;
-      s.b0 = cur.w.b0 + cur.pair * 2 * TQ;
-      s.b1 = min(cur.w.b1, s.b0 + 2 * TQ);
-      s.b_table = b_table;
-      s.head = cur.head;
-      s.rows = (s.b1 - s.b0) * G;
-      s.prefix = cur.w.prefix;
-      s.tile0 = cur.tile;
-      // tiles whose last step lies before the range's end
-      s.tile1 = (int)min((int64_t)cur.w.tiles, (x_end - cur.item_x) / w);
-      if (b_table < 0) s.tile1 = s.tile0;  // nobody to read the result
-      const int64_t base = 2 * ((int64_t)p.num_kv_heads * cur.w.b0 * G +
-                                (int64_t)cur.head * (cur.w.b1 - cur.w.b0) * G +
-                                (int64_t)cur.pair * kPairRows);
-      const int64_t row = base + (int64_t)kPairRows * blockIdx.x;
-      // Items of one CTA lie 2 * rows apart, parts of an item kPairRows: no two
-      // segments overlap, and the last ends by 2 * batch * heads + kPairRows * CTAs.
-      s.row_base = (int32_t)row;
-      if (s.tile0 == 0 && s.tile1 > 0) {
-        const int64_t c0 = cta_of(cur.item_x + w - 1, Ce, T);
-        const int64_t c1 = cta_of(cur.item_x + (int64_t)cur.w.tiles * w - 1, Ce, T);
-        const int4 info =
-            make_int4((int)(base + kPairRows * c0), (int)(c1 - c0 + 1), s.b0, s.rows);
-        for (int b = s.b0; b < s.b1; ++b)
-          sp.pre_info[(int64_t)b * p.num_kv_heads + s.head] = info;
-      }
-      ct.seg = s;
-    }
-    __syncthreads();
-    if (!ct.more || ct.abort) break;
-    const Segment sg = ct.seg;
-    const int n = max(sg.tile1 - sg.tile0, 0);     // key tiles
-    const bool pairs = sg.rows > kRows;            // two Q tiles
-    const int nsteps = pairs ? 2 * n : n;
-    const int steps_x[2] = {(nsteps + 1) >> 1, nsteps >> 1};
+  if (warp < 8) {
+    if constexpr (quant(kFmt)) set_registers<kSoftmaxRegs, true>();
+    // ------------------------------------------------------------- softmax
+    const int x = warp >> 2;   // slot
+    const int wq = warp & 3;   // TMEM lane quadrant of this warp
+    const int r = wq * 32 + lane;  // row of the tile = TMEM lane
+    const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+    const uint32_t colS = col_s(x), colO = col_o(x);
+    uint32_t j0 = 0, steps = 0, outs = 0;  // key tiles, steps and O tiles so far
     bool ok = true;
-
-    if (n > 0 && warp == kProducerWarp) {
-      // ---------------------------------------------------------- producer
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&ct.q_full, (uint32_t)(pairs ? 2 : 1) * Sm::kQB);
-        for (int x = 0; x < (pairs ? 2 : 1); ++x)
-#pragma unroll
-          for (int h = 0; h < Sm::kHalves; ++h)
-            tma_load_3d(sq + x * Sm::kQB + h * (kRows * 128), &tmap_q, h * 64, sg.head * G,
-                        sg.b0 + x * TQ, &ct.q_full);
-        const uint64_t pol = policy_evict_first();
-        // bytes of one operand (K or V) per live 64-key block
-        constexpr uint32_t kBlockBytes =
-            quant(kFmt) ? 64u * (Sm::kCodeRowB + Sm::kScaleRowB) : Sm::kHalves * 64u * 128u;
-        for (int i = 0; i < n; ++i) {
-          const uint32_t j = jbase + i;
-          const int st = j % kStages;
-          const uint32_t ph = (j / kStages - 1) & 1;
-          // page lookup: page ids, scales, rejected 64-key blocks
-          TileFacts tf;
-          tf.bad = 0;
-          int live = 0;
-          int32_t ys[2] = {0, 0};
-          for (int sb = 0; sb < 2; ++sb) {
-            tf.ks[sb] = tf.vs[sb] = 1.f;
-            const int32_t key0 = (sg.tile0 + i) * kKeys + sb * 64;
-            if (key0 >= sg.prefix) continue;
-            const int32_t pid =
-                __ldg(p.page_table + (int64_t)sg.b_table * p.max_pages + key0 / p.page_size);
-            if (pid < 0 || pid >= p.num_pages) {
-              flag_error(p.flags, PKV_FLAG_BAD_PAGE);
-              tf.bad |= 1 << sb;
-              continue;
-            }
-            if constexpr (quant(kFmt)) {
-              const float ks = __ldg(p.k_scale + (int64_t)pid * p.num_kv_heads + sg.head);
-              const float vs = __ldg(p.v_scale + (int64_t)pid * p.num_kv_heads + sg.head);
-              if (!(ks > 0.f && ks <= 32768.f && vs > 0.f && vs <= 32768.f)) {
-                flag_error(p.flags, PKV_FLAG_BAD_SCALE);
-                tf.bad |= 1 << sb;
-                continue;
-              }
-              tf.ks[sb] = ks;
-              tf.vs[sb] = vs;
-            }
-            ys[sb] = (int32_t)(((int64_t)pid * p.num_kv_heads + sg.head) * p.page_size +
-                               key0 % p.page_size);
-            live |= 1 << sb;
-          }
-          auto load = [&](const CUtensorMap* map, const uint8_t* blocks, uint8_t* dst,
-                          uint64_t* bar) {
-            mbar_arrive_expect_tx(bar, (uint32_t)__popc(live) * kBlockBytes);
-            for (int sb = 0; sb < 2; ++sb) {
-              if (!((live >> sb) & 1)) continue;
-              if constexpr (quant(kFmt)) {
-                tma_load_2d(dst + sb * 64 * Sm::kCodeRowB, map, 0, ys[sb], bar, pol);
-                if constexpr (fp4(kFmt))
-                  bulk_load(dst + Sm::kCodesB + sb * 64 * Sm::kScaleRowB,
-                            blocks + (int64_t)ys[sb] * Sm::kScaleRowB, 64u * Sm::kScaleRowB, bar);
-              } else {
-#pragma unroll
-                for (int h = 0; h < Sm::kHalves; ++h)
-                  tma_load_2d(dst + h * Sm::kHalfB + sb * 64 * 128, map, h * 64, ys[sb], bar,
-                              pol);
-              }
-            }
-          };
-          uint8_t* kd = skv + st * Sm::kStageB;
-          if (j >= kStages && !mbar_wait(&ct.k_empty[st], ph, p.flags)) { ok = false; break; }
-          ct.facts[j % kFactsRing] = tf;
-          mbar_arrive(&ct.facts_full[j % kFactsRing]);
-          load(&tmap_k, p.k_blocks, kd, &ct.k_full[st]);
-          if (j >= kStages && !mbar_wait(&ct.v_empty[st], ph, p.flags)) { ok = false; break; }
-          load(&tmap_v, p.v_blocks, kd + Sm::kStageB / 2, &ct.v_full[st]);
-        }
-        // every load has landed before the segment ends (the CTA may end then)
-        for (int i = max(0, n - kStages); i < n && ok; ++i) {
-          const uint32_t j = jbase + i;
-          ok = mbar_wait(&ct.k_full[j % kStages], (j / kStages) & 1, p.flags) &&
-               mbar_wait(&ct.v_full[j % kStages], (j / kStages) & 1, p.flags);
-        }
-        if (!ok) ct.abort = 1;
-      }
-    } else if (n > 0 && quant(kFmt) && warp >= kConvWarp0) {
-      // -------------------------------------------- codes -> 16-bit converters
-      const int t = threadIdx.x - kConvWarp0 * 32;
-      const uint32_t kc = smem_u32(sconv), vc = kc + Sm::kTileB;
-      for (int i = 0; i < n; ++i) {
-        const uint32_t j = jbase + i;
-        const int st = j % kStages;
-        const uint32_t par = (j / kStages) & 1;
-        if (!mbar_wait(&ct.k_full[st], par, p.flags)) { ok = false; break; }
-        const uint32_t k_codes = smem_u32(skv + st * Sm::kStageB);
-        const uint32_t v_codes = k_codes + Sm::kStageB / 2;
-        const int bad = ct.facts[j % kFactsRing].bad;
-        const int32_t key0 = (sg.tile0 + i) * kKeys;
-        const int zero_from = key0 + kKeys > sg.prefix ? max(0, sg.prefix - key0) : kKeys;
-        if (j >= 1 && !mbar_wait(&ct.kc_free, (j - 1) & 1, p.flags)) { ok = false; break; }
-        if constexpr (fp4(kFmt))
-          convert_fp4_tile<D, false, kConvThreads>(k_codes, kc, t, zero_from, bad);
-        else
-          convert_tile<D, kFmt, false, kConvThreads>(k_codes, kc, t, zero_from, bad);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ct.kc_full);
-          mbar_arrive(&ct.k_empty[st]);
-        }
-        if (!mbar_wait(&ct.v_full[st], par, p.flags)) { ok = false; break; }
-        if (j >= 1 && !mbar_wait(&ct.vc_free, (j - 1) & 1, p.flags)) { ok = false; break; }
-        if constexpr (fp4(kFmt))
-          convert_fp4_tile<D, true, kConvThreads>(v_codes, vc, t, zero_from, bad);
-        else
-          convert_tile<D, kFmt, true, kConvThreads>(v_codes, vc, t, zero_from, bad);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ct.vc_full);
-          mbar_arrive(&ct.v_empty[st]);
-        }
-      }
-      if (!ok) ct.abort = 1;
-    } else if (n > 0 && warp == kMmaWarp) {
-      // --------------------------------------------------------------- MMA
-      const uint32_t id_s = idesc_f16kind(kRows, kKeys, 0, true);
-      const uint32_t id_o = idesc_f16kind(kRows, D, 1, !quant(kFmt));
-      const uint32_t q_addr = smem_u32(sq);
-      ok = mbar_wait(&ct.q_full, nseg & 1, p.flags);
-      // local tile of step s, and whether the step is its tile's first / last
-      auto tile_of = [&](int s) { return pairs ? s >> 1 : s; };
-      auto first_of = [&](int s) { return !pairs || !(s & 1); };
-      auto last_of = [&](int s) { return !pairs || (s & 1); };
-      uint32_t k_addr = 0, v_addr = 0;
-      // S of step s: wait for its K tile, issue, release the tile after its last step
-      auto issue_s = [&](int s) -> bool {
-        const uint32_t j = jbase + tile_of(s);
-        if (first_of(s)) {
-          if constexpr (quant(kFmt)) {
-            k_addr = smem_u32(sconv);
-            if (!mbar_wait(&ct.kc_full, j & 1, p.flags)) return false;
-          } else {
-            k_addr = smem_u32(skv + (j % kStages) * Sm::kStageB);
-            if (!mbar_wait(&ct.k_full[j % kStages], (j / kStages) & 1, p.flags)) return false;
-          }
-        }
-        const int x = s & 1;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t qa = q_addr + (pairs ? x * Sm::kQB : 0);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const int h = kk >> 2, w = kk & 3;
-            const uint64_t ad = sdesc(qa + h * (kRows * 128) + w * 32, 16, 1024);
-            const uint64_t bd = sdesc(k_addr + h * Sm::kHalfB + w * 32, 16, 1024);
-            mma_ss(tmem + col_s(x), ad, bd, id_s, kk > 0 ? 1u : 0u);
-          }
-          tc_commit(&ct.s_full[x]);
-          if (last_of(s)) tc_commit(quant(kFmt) ? &ct.kc_free : &ct.k_empty[j % kStages]);
-        }
-        __syncwarp();
-        return true;
-      };
-      // O += P V of step s; V rows past the end or of a rejected page are zeroed
-      auto issue_pv = [&](int s) -> bool {
-        const uint32_t j = jbase + tile_of(s);
-        if (first_of(s)) {
-          if constexpr (quant(kFmt)) {
-            v_addr = smem_u32(sconv) + Sm::kTileB;
-            if (!mbar_wait(&ct.vc_full, j & 1, p.flags)) return false;
-          } else {
-            const int st = j % kStages;
-            if (!mbar_wait(&ct.v_full[st], (j / kStages) & 1, p.flags)) return false;
-            const int32_t key0 = (sg.tile0 + tile_of(s)) * kKeys;
-            const int bad = ct.facts[j % kFactsRing].bad;
-            const int zlo = key0 + kKeys > sg.prefix ? max(0, sg.prefix - key0) : kKeys;
-            uint8_t* vd = skv + st * Sm::kStageB + Sm::kTileB;
-            if (zlo < kKeys || bad) {
-              for (int idx = lane; idx < kKeys * Sm::kHalves * 8; idx += 32) {
-                const int row = idx / (Sm::kHalves * 8);
-                const int rem = idx - row * (Sm::kHalves * 8);
-                const int h = rem >> 3, c = rem & 7;
-                if (row >= zlo || ((bad >> (row >> 6)) & 1))
-                  *reinterpret_cast<uint4*>(vd + h * Sm::kHalfB + row * 128 + c * 16) =
-                      make_uint4(0, 0, 0, 0);
-              }
-              fence_async_smem();
-              __syncwarp();
-            }
-            v_addr = smem_u32(vd);
-          }
-        }
-        const int x = s & 1;
-        if (!mbar_wait(&ct.p_full[x], (cbase[x] + (s >> 1)) & 1, p.flags)) return false;
-        tc_fence_after();
-        if (lane == 0) {
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk) {
-            const uint64_t bd = sdesc(v_addr + kk * 2048, Sm::kHalfB, 1024);
-            mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, bd, id_o,
-                   (s >= 2 || kk > 0) ? 1u : 0u);
-          }
-          tc_commit(&ct.o_bar[x]);
-          if (last_of(s)) tc_commit(quant(kFmt) ? &ct.vc_free : &ct.v_empty[j % kStages]);
-        }
-        __syncwarp();
-        return true;
-      };
-      if (ok) ok = issue_s(0);
-      if (ok && nsteps > 1) ok = issue_s(1);
-      for (int s = 0; s < nsteps && ok; ++s) {
-        if (!(ok = issue_pv(s))) break;
-        if (s + 2 < nsteps) ok = issue_s(s + 2);
-      }
-      if (!ok) ct.abort = 1;
-    } else if (n > 0 && warp < 8) {
-      // ----------------------------------------------------------- softmax
-      const int x = warp >> 2;   // slot
-      const int wq = warp & 3;   // TMEM lane quadrant of this warp
-      const int r = wq * 32 + lane;  // row of the tile = TMEM lane
-      const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
-      const uint32_t colS = col_s(x), colO = col_o(x);
-      const int b = sg.b0 + (pairs ? x * TQ : 0) + r / G;
-      const bool row_ok = b < sg.b1;
+    Segment sg;
+    for (uint32_t k = 0; ok && take_segment(k, &sg); ++k) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ct.seg_empty[k % kSegRing]);
+      const bool pairs = sg.rows > kRows;
+      const int mine = pairs ? sg.n : (sg.n + 1 - x) >> 1;  // steps of this slot
       float m_ref = -INFINITY, l = 0.f;
-      const int mine = x ? steps_x[1] : steps_x[0];
-      const uint32_t c0 = x ? cbase[1] : cbase[0];
+      float row_mul = p.scale_log2;
+      if (quant(kFmt) && mine > 0) {
+        if (!mbar_wait(&ct.qc_full, k & 1, p.flags)) { ok = false; break; }
+        row_mul = ldexpf(p.scale_log2, -ct.q_exp[k & 1][pairs ? x : 0][r]);
+      }
       for (int q = 0; q < mine; ++q) {
         const int i = pairs ? q : 2 * q + x;  // local key tile
-        const uint32_t j = jbase + i;
-        if (!mbar_wait(&ct.s_full[x], (c0 + q) & 1, p.flags) ||
+        const uint32_t j = j0 + i;
+        if (!mbar_wait(&ct.s_full[x], (steps + q) & 1, p.flags) ||
             !mbar_wait(&ct.facts_full[j % kFactsRing], (j / kFactsRing) & 1, p.flags)) {
           ok = false;
           break;
@@ -562,8 +405,8 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         const TileFacts tf = ct.facts[j % kFactsRing];
         tc_fence_after();
         const int32_t key0 = (sg.tile0 + i) * kKeys;
-        const float mul0 = quant(kFmt) ? p.scale_log2 * tf.ks[0] : p.scale_log2;
-        const float mul1 = quant(kFmt) ? p.scale_log2 * tf.ks[1] : p.scale_log2;
+        const float mul0 = quant(kFmt) ? row_mul * tf.ks[0] : row_mul;
+        const float mul1 = quant(kFmt) ? row_mul * tf.ks[1] : row_mul;
         // Quantised pools: the V scale of a 64-key block rides on P as an
         // exponent, P = 2^(s - m + log2 vs), and m bounds s + log2 vs, so that
         // the f16 P keeps its 11 bits whatever the scales are; the row sum takes
@@ -656,66 +499,394 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       // Rows of slot x: float4 vectors [D/4][rows of the slot], so that a warp's
       // lanes write consecutive 16 bytes; (m, l) beside them.  For quantised
       // pools o takes l's unit, and m makes up for it.
+      if (!ok) break;
       constexpr float kUnit = quant(kFmt) ? kSumUnit : 1.f;
-      const int nr0 = min(sg.rows, kRows);  // rows of slot 0's Q tile
-      const int nr = pairs ? (x ? sg.rows - kRows : kRows) : sg.rows;
-      const bool out_ok = row_ok && r < nr;
-      if (ok && mine > 0 &&
-          !mbar_wait(&ct.o_bar[x], (c0 + mine - 1) & 1, p.flags))
-        ok = false;
-      if (ok) {
+      const int nr = pairs ? (x ? sg.rows - kRows : kRows) : sg.rows;  // rows of the slot
+      const bool out_ok = r < nr;
+      const int64_t row0 = (int64_t)sg.row_base + (x ? min(sg.rows, kRows) : 0);
+      // (no step or no live key: l = 0; NaN passes)
+      if (out_ok) sp.pre_ml[row0 + r] = make_float2(m_ref + (quant(kFmt) ? 60.f : 0.f), l);
+      if (mine > 0) {
+        if (!mbar_wait(&ct.o_full[x], outs & 1, p.flags)) { ok = false; break; }
+        ++outs;
         tc_fence_after();
-        const int64_t row0 = (int64_t)sg.row_base + (x ? nr0 : 0);
-        if (mine > 0) {
-          float4* dst = reinterpret_cast<float4*>(sp.pre_o) + row0 * (D / 4) + r;
+        float4* dst = reinterpret_cast<float4*>(sp.pre_o) + row0 * (D / 4) + r;
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32(tmem + lane_base + colO + c, o);
-            tmem_wait_ld();
-            if (out_ok) {
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(tmem + lane_base + colO + c, o);
+          tmem_wait_ld();
+          if (out_ok) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                dst[(int64_t)((c + e) / 4) * nr] = make_float4(o[e] * kUnit, o[e + 1] * kUnit,
-                                                               o[e + 2] * kUnit, o[e + 3] * kUnit);
-            }
+            for (int e = 0; e < 32; e += 4)
+              dst[(int64_t)((c + e) / 4) * nr] = make_float4(o[e] * kUnit, o[e + 1] * kUnit,
+                                                             o[e + 2] * kUnit, o[e + 3] * kUnit);
           }
         }
-        // (no step or no live key: l = 0; NaN passes)
-        if (out_ok) sp.pre_ml[row0 + r] = make_float2(m_ref + (quant(kFmt) ? 60.f : 0.f), l);
-      } else {
-        ct.abort = 1;
       }
+      steps += mine;
+      j0 += sg.n;
     }
-
-    // ------------------------------------------------------ end of a segment
-    jbase += n;
-    cbase[0] += steps_x[0];
-    cbase[1] += steps_x[1];
-    if (n > 0) ++nseg;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 0) {
-      // the next item, if the range reaches into it
-      const int w = pair_tiles(cur.w, cur.pair);
-      const int64_t next_x = cur.item_x + (int64_t)cur.w.tiles * w;
-      more = next_x < x_end;
-      if (more) cur = locate(p, next_x, lane);
-      if (lane == 0) ct.more = more ? 1 : 0;
+  } else {
+    if constexpr (quant(kFmt)) set_registers<kOtherRegs, false>();
+    if (warp == kSchedWarp) {
+      // ------------------------------------------------------------ scheduler
+      // This CTA's range of the work list, one descriptor per item it reaches.
+      bool pairs = false;
+      const int64_t T = total_steps(p, lane, &pairs);
+      // Every range holds a whole tile (two steps of an item with two Q tiles).
+      int64_t Ce = min((int64_t)gridDim.x, pairs ? T / 2 : T);
+      if (Ce < 1) Ce = 1;
+      const int64_t c = blockIdx.x;
+      if (c == 0)
+        for (int g = lane; g < p.num_groups; g += 32) {
+          const int32_t b0 = __ldg(p.cu_groups + g), b1 = __ldg(p.cu_groups + g + 1);
+          if (b0 < 0 || b1 < b0 || b1 > p.batch || __ldg(p.prefix_lens + g) < 0)
+            flag_error(p.flags, PKV_FLAG_BAD_LENGTH);
+        }
+      const int64_t x_end = (c + 1) * T / Ce;
+      int64_t x = c < Ce ? c * T / Ce : x_end;
+      uint32_t k = 0;
+      while (true) {
+        Segment s{};
+        if (x < x_end) {
+          const Cursor cur = locate(p, x, lane);
+          const int b_table = first_holder(p, cur.w, lane);
+          const int w = pair_tiles(cur.w, cur.pair);
+          s.b0 = cur.w.b0 + cur.pair * 2 * TQ;
+          s.b1 = min(cur.w.b1, s.b0 + 2 * TQ);
+          s.b_table = b_table;
+          s.head = cur.head;
+          s.rows = (s.b1 - s.b0) * G;
+          s.prefix = cur.w.prefix;
+          s.tile0 = cur.tile;
+          // tiles whose last step lies before the range's end
+          s.n = (int)min((int64_t)cur.w.tiles, (x_end - cur.item_x) / w) - s.tile0;
+          if (b_table < 0) s.n = 0;  // nobody to read the result
+          // Items of one CTA lie 2 * rows apart, parts of an item kPairRows: no two
+          // segments overlap, and the last ends by 2 * batch * heads + kPairRows * CTAs.
+          const int64_t base = 2 * ((int64_t)p.num_kv_heads * cur.w.b0 * G +
+                                    (int64_t)cur.head * (cur.w.b1 - cur.w.b0) * G +
+                                    (int64_t)cur.pair * kPairRows);
+          s.row_base = (int32_t)(base + (int64_t)kPairRows * c);
+          if (s.tile0 == 0 && s.n > 0) {
+            const int64_t c0 = cta_of(cur.item_x + w - 1, Ce, T);
+            const int64_t c1 = cta_of(cur.item_x + (int64_t)cur.w.tiles * w - 1, Ce, T);
+            const int4 info =
+                make_int4((int)(base + kPairRows * c0), (int)(c1 - c0 + 1), s.b0, s.rows);
+            for (int b = s.b0 + lane; b < s.b1; b += 32)
+              sp.pre_info[(int64_t)b * p.num_kv_heads + s.head] = info;
+          }
+          x = cur.item_x + (int64_t)cur.w.tiles * w;
+          if (s.n <= 0) continue;
+        }
+        if (!mbar_wait(&ct.seg_empty[k % kSegRing], ((k / kSegRing) & 1) ^ 1, p.flags)) break;
+        if (lane == 0) {
+          ct.seg[k % kSegRing] = s;
+          mbar_arrive(&ct.seg_full[k % kSegRing]);
+        }
+        __syncwarp();
+        ++k;
+        if (s.n == 0) break;
+      }
+    } else if (warp == kProducerWarp) {
+      // ------------------------------------------------------------- producer
+      if (lane == 0) {
+        tma_prefetch_desc(&tmap_q);
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+        const uint64_t pol = policy_evict_first();
+        // bytes of one operand (K or V) per live 64-key block
+        constexpr uint32_t kBlockBytes =
+            quant(kFmt) ? 64u * (Sm::kCodeRowB + Sm::kScaleRowB) : Sm::kHalves * 64u * 128u;
+        Ring ring;
+        uint32_t j = 0, used = 0;  // key tiles so far; slots with a fill
+        bool ok = true;
+        Segment sg;
+        for (uint32_t k = 0; ok && take_segment(k, &sg); ++k) {
+          mbar_arrive(&ct.seg_empty[k % kSegRing]);
+          const bool pairs = sg.rows > kRows;
+          const int depth = ring_depth(pairs);
+          ring.enter(depth);
+          // page lookup of tile i: page ids, scales, rejected 64-key blocks
+          struct Lookup {
+            TileFacts tf;
+            int32_t ys[2];
+            int live;
+          };
+          auto lookup = [&](int i) -> Lookup {
+            Lookup lk;
+            lk.tf.bad = 0;
+            lk.live = 0;
+            for (int sb = 0; sb < 2; ++sb) {
+              lk.tf.ks[sb] = lk.tf.vs[sb] = 1.f;
+              lk.ys[sb] = 0;
+              const int32_t key0 = (sg.tile0 + i) * kKeys + sb * 64;
+              if (key0 >= sg.prefix) continue;
+              const int32_t pid =
+                  __ldg(p.page_table + (int64_t)sg.b_table * p.max_pages + key0 / p.page_size);
+              if (pid < 0 || pid >= p.num_pages) {
+                flag_error(p.flags, PKV_FLAG_BAD_PAGE);
+                lk.tf.bad |= 1 << sb;
+                continue;
+              }
+              if constexpr (quant(kFmt)) {
+                const float ks = __ldg(p.k_scale + (int64_t)pid * p.num_kv_heads + sg.head);
+                const float vs = __ldg(p.v_scale + (int64_t)pid * p.num_kv_heads + sg.head);
+                if (!(ks > 0.f && ks <= 32768.f && vs > 0.f && vs <= 32768.f)) {
+                  flag_error(p.flags, PKV_FLAG_BAD_SCALE);
+                  lk.tf.bad |= 1 << sb;
+                  continue;
+                }
+                lk.tf.ks[sb] = ks;
+                lk.tf.vs[sb] = vs;
+              }
+              lk.ys[sb] = (int32_t)(((int64_t)pid * p.num_kv_heads + sg.head) * p.page_size +
+                                    key0 % p.page_size);
+              lk.live |= 1 << sb;
+            }
+            return lk;
+          };
+          auto load = [&](const CUtensorMap* map, const uint8_t* blocks, uint8_t* dst,
+                          uint64_t* bar, const Lookup& lk) {
+            mbar_arrive_expect_tx(bar, (uint32_t)__popc(lk.live) * kBlockBytes);
+            for (int sb = 0; sb < 2; ++sb) {
+              if (!((lk.live >> sb) & 1)) continue;
+              if constexpr (quant(kFmt)) {
+                tma_load_2d(dst + sb * 64 * Sm::kCodeRowB, map, 0, lk.ys[sb], bar, pol);
+                if constexpr (fp4(kFmt))
+                  bulk_load(dst + Sm::kCodesB + sb * 64 * Sm::kScaleRowB,
+                            blocks + (int64_t)lk.ys[sb] * Sm::kScaleRowB, 64u * Sm::kScaleRowB, bar);
+              } else {
+  #pragma unroll
+                for (int h = 0; h < Sm::kHalves; ++h)
+                  tma_load_2d(dst + h * Sm::kHalfB + sb * 64 * 128, map, h * 64, lk.ys[sb], bar,
+                              pol);
+              }
+            }
+          };
+          Lookup cur = lookup(0);
+          for (int i = 0; i < sg.n; ++i, ++j) {
+            const int st = ring.slot;
+            const uint32_t free_parity = ring.parity() ^ 1;
+            if (!mbar_wait(&ct.k_empty[st], free_parity, p.flags)) { ok = false; break; }
+            ct.facts[j % kFactsRing] = cur.tf;
+            mbar_arrive(&ct.facts_full[j % kFactsRing]);
+            load(&tmap_k, p.k_blocks, k_slot(st), &ct.k_full[st], cur);
+            if (i == 0) {  // the queries: behind the last S of the segment before
+              if (!mbar_wait(&ct.q_empty, (k & 1) ^ 1, p.flags)) {
+                ok = false;
+                mbar_wait(&ct.k_full[st], ring.parity(), p.flags);  // let the load land
+                break;
+              }
+              mbar_arrive_expect_tx(&ct.q_full, (uint32_t)(pairs ? 2 : 1) * Sm::kQB);
+              for (int x = 0; x < (pairs ? 2 : 1); ++x)
+  #pragma unroll
+                for (int h = 0; h < Sm::kHalves; ++h)
+                  tma_load_3d(sq + x * Sm::kQB + h * (kRows * 128), &tmap_q, h * 64, sg.head * G,
+                              sg.b0 + x * TQ, &ct.q_full);
+            }
+            if (!mbar_wait(&ct.v_empty[st], free_parity, p.flags)) { ok = false; break; }
+            load(&tmap_v, p.v_blocks, v_slot(st), &ct.v_full[st], cur);
+            used |= 1u << st;
+            ring.advance(depth);
+            if (i + 1 < sg.n) cur = lookup(i + 1);  // ahead of the next slot wait
+          }
+        }
+        // No copy may be on its way to this CTA's shared memory when it ends.  (One
+        // issued before a wait that gave up had that wait's whole limit to land.)
+        for (int st = 0; st <= Sm::kStages; ++st)
+          if ((used >> st) & 1) {
+            mbar_wait(&ct.k_full[st], ((ring.parities >> st) & 1) ^ 1, p.flags);
+            mbar_wait(&ct.v_full[st], ((ring.parities >> st) & 1) ^ 1, p.flags);
+          }
+      }
+    } else if (quant(kFmt) && warp >= kConvWarp0) {
+      // ------------------------------------------- codes -> f16 converters
+      const int t = threadIdx.x - kConvWarp0 * 32;
+      const uint32_t kc = smem_u32(sconv), vc = kc + Sm::kTileB;
+      Ring ring;
+      uint32_t j = 0;
+      bool ok = true;
+      Segment sg;
+      for (uint32_t k = 0; ok && take_segment(k, &sg); ++k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ct.seg_empty[k % kSegRing]);
+        const bool pairs = sg.rows > kRows;
+        const int depth = ring_depth(pairs);
+        ring.enter(depth);
+        // Q to f16 in place, a row a thread, times the power of two that puts the
+        // row's largest value in [2^14, 2^15): bf16's 8 bits fit f16's 11, and what
+        // is small enough to lose bits is 2^-28 of the largest.
+        if (!mbar_wait(&ct.q_full, k & 1, p.flags)) break;
+        for (int x = 0; x < (pairs ? 2 : 1); ++x)
+          ct.q_exp[k & 1][x][t] = (int8_t)q_row_to_f16<D>(smem_u32(sq) + x * Sm::kQB, t);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ct.qc_full);
+        for (int i = 0; i < sg.n; ++i, ++j) {
+          const int st = ring.slot;
+          const uint32_t par = ring.parity();
+          if (!mbar_wait(&ct.k_full[st], par, p.flags)) { ok = false; break; }
+          const uint32_t k_codes = smem_u32(k_slot(st)), v_codes = smem_u32(v_slot(st));
+          const int bad = ct.facts[j % kFactsRing].bad;
+          const int32_t key0 = (sg.tile0 + i) * kKeys;
+          const int zero_from = min(kKeys, sg.prefix - key0);
+          if (!mbar_wait(&ct.kc_free, (j & 1) ^ 1, p.flags)) { ok = false; break; }
+          if constexpr (fp4(kFmt))
+            convert_fp4_tile<D, true, kConvThreads>(k_codes, kc, t, zero_from, bad);
+          else
+            convert_tile<D, kFmt, true, kConvThreads>(k_codes, kc, t, zero_from, bad);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ct.kc_full);
+            mbar_arrive(&ct.k_empty[st]);
+          }
+          if (!mbar_wait(&ct.v_full[st], par, p.flags)) { ok = false; break; }
+          if (!mbar_wait(&ct.vc_free, (j & 1) ^ 1, p.flags)) { ok = false; break; }
+          if constexpr (fp4(kFmt))
+            convert_fp4_tile<D, true, kConvThreads>(v_codes, vc, t, zero_from, bad);
+          else
+            convert_tile<D, kFmt, true, kConvThreads>(v_codes, vc, t, zero_from, bad);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ct.vc_full);
+            mbar_arrive(&ct.v_empty[st]);
+          }
+          ring.advance(depth);
+        }
+      }
+    } else if (warp == kMmaWarp) {
+      // ----------------------------------------------------------------- MMA
+      const uint32_t id_s = idesc_f16kind(kRows, kKeys, 0, !quant(kFmt));
+      const uint32_t id_o = idesc_f16kind(kRows, D, 1, !quant(kFmt));
+      const uint32_t q_addr = smem_u32(sq);
+      Ring kring, vring;        // bf16: slots of the next K and V tile
+      uint32_t jk = 0, jv = 0;  // key tiles so far, as S and as PV sees them
+      uint32_t steps[2] = {0, 0};  // of each slot, before this segment
+      uint32_t k_addr = 0, v_addr = 0;
+      bool ok = true;
+      Segment sg;
+      for (uint32_t k = 0; ok && take_segment(k, &sg); ++k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ct.seg_empty[k % kSegRing]);
+        const bool pairs = sg.rows > kRows;
+        const int depth = ring_depth(pairs);
+        kring.enter(depth);
+        vring.enter(depth);
+        const int nsteps = pairs ? 2 * sg.n : sg.n;
+        // whether a step is its tile's first / last
+        auto first_of = [&](int s) { return !pairs || !(s & 1); };
+        auto last_of = [&](int s) { return !pairs || (s & 1); };
+        // S of step s: wait for its K tile, issue, release the tile after its last step
+        auto issue_s = [&](int s) -> bool {
+          if (first_of(s)) {
+            if constexpr (quant(kFmt)) {
+              k_addr = smem_u32(sconv);
+              if (!mbar_wait(&ct.kc_full, jk & 1, p.flags)) return false;
+            } else {
+              k_addr = smem_u32(k_slot(kring.slot));
+              if (!mbar_wait(&ct.k_full[kring.slot], kring.parity(), p.flags)) return false;
+            }
+          }
+          const int x = s & 1;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t qa = q_addr + (pairs ? x * Sm::kQB : 0);
+  #pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const int h = kk >> 2, w = kk & 3;
+              const uint64_t ad = sdesc(qa + h * (kRows * 128) + w * 32, 16, 1024);
+              const uint64_t bd = sdesc(k_addr + h * Sm::kHalfB + w * 32, 16, 1024);
+              mma_ss(tmem + col_s(x), ad, bd, id_s, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(&ct.s_full[x]);
+            if (last_of(s)) tc_commit(quant(kFmt) ? &ct.kc_free : &ct.k_empty[kring.slot]);
+            if (s == nsteps - 1) tc_commit(&ct.q_empty);
+          }
+          __syncwarp();
+          if (last_of(s)) {
+            kring.advance(depth);
+            ++jk;
+          }
+          return true;
+        };
+        // O += P V of step s; V rows past the end or of a rejected page are zeroed
+        auto issue_pv = [&](int s) -> bool {
+          if (first_of(s)) {
+            if constexpr (quant(kFmt)) {
+              v_addr = smem_u32(sconv) + Sm::kTileB;
+              if (!mbar_wait(&ct.vc_full, jv & 1, p.flags)) return false;
+            } else {
+              if (!mbar_wait(&ct.v_full[vring.slot], vring.parity(), p.flags)) return false;
+              const int32_t key0 = (sg.tile0 + (pairs ? s >> 1 : s)) * kKeys;
+              const int bad = ct.facts[jv % kFactsRing].bad;
+              const int zlo = min(kKeys, sg.prefix - key0);
+              uint8_t* vd = v_slot(vring.slot);
+              if (zlo < kKeys || bad) {
+                for (int idx = lane; idx < kKeys * Sm::kHalves * 8; idx += 32) {
+                  const int row = idx / (Sm::kHalves * 8);
+                  const int rem = idx - row * (Sm::kHalves * 8);
+                  const int h = rem >> 3, c = rem & 7;
+                  if (row >= zlo || ((bad >> (row >> 6)) & 1))
+                    *reinterpret_cast<uint4*>(vd + h * Sm::kHalfB + row * 128 + c * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+                __syncwarp();
+              }
+              v_addr = smem_u32(vd);
+            }
+          }
+          const int x = s & 1;
+          if (!mbar_wait(&ct.p_full[x], (steps[x] + (s >> 1)) & 1, p.flags)) return false;
+          tc_fence_after();
+          if (lane == 0) {
+  #pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk) {
+              const uint64_t bd = sdesc(v_addr + kk * 2048, Sm::kHalfB, 1024);
+              mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, bd, id_o,
+                     (s >= 2 || kk > 0) ? 1u : 0u);
+            }
+            if (last_of(s)) tc_commit(quant(kFmt) ? &ct.vc_free : &ct.v_empty[vring.slot]);
+            if (s + 2 >= nsteps) tc_commit(&ct.o_full[x]);  // the slot's last step
+          }
+          __syncwarp();
+          if (last_of(s)) {
+            vring.advance(depth);
+            ++jv;
+          }
+          return true;
+        };
+        if (quant(kFmt))
+          ok = mbar_wait(&ct.qc_full, k & 1, p.flags);
+        else
+          ok = mbar_wait(&ct.q_full, k & 1, p.flags);
+        if (ok) ok = issue_s(0);
+        if (ok && nsteps > 1) ok = issue_s(1);
+        for (int s = 0; s < nsteps && ok; ++s) {
+          if (!(ok = issue_pv(s))) break;
+          if (s + 2 < nsteps) ok = issue_s(s + 2);
+        }
+        steps[0] += (nsteps + 1) >> 1;
+        steps[1] += nsteps >> 1;
+      }
+      // every MMA this thread issued must finish before TMEM is released
+      if (lane == 0) tc_commit(&ct.done);
+      __syncwarp();
     }
   }
 
   // ------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
   if (warp == kMmaWarp) {
-    if (lane == 0) tc_commit(&ct.done_bar);
-    __syncwarp();
-    mbar_wait(&ct.done_bar, 0, p.flags);
     tc_fence_after();
+    mbar_wait(&ct.done, 0, p.flags);
     tmem_dealloc(tmem, kTmemCols);
   }
-  // (A producer whose wait gave up issued its last load before that wait, whose
-  // whole limit the load had to land.)
 }
 
 // ------------------------------------------------------------------- merge
@@ -906,7 +1077,7 @@ cudaError_t merge_for(const SharedParams& sp, cudaStream_t stream) {
 template <int D, int kFmt>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const SharedParams& p, int num_ctas, cudaStream_t stream) {
-  const size_t smem = 1024 + Smem<D, kFmt>::kBytes + sizeof(Control);
+  const size_t smem = Smem<D, kFmt>::kBytes;
   // The shared-memory attribute belongs to the current device: set it once
   // per device and instantiation.
   constexpr int kMaxDevices = 64;
@@ -919,6 +1090,10 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!attr[dev]) {
+      // The register exchange counts on what the block is launched with.
+      cudaFuncAttributes fa;
+      if ((e = cudaFuncGetAttributes(&fa, prefix_kernel<D, kFmt>)) != cudaSuccess) return e;
+      if (quant(kFmt) && fa.numRegs != kLaunchRegs) return cudaErrorLaunchOutOfResources;
       e = cudaFuncSetAttribute(prefix_kernel<D, kFmt>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (e != cudaSuccess) return e;
