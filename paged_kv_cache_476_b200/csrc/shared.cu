@@ -66,13 +66,14 @@ constexpr float kTiny = 1.17549435e-38f;       // smallest normal fp32
 constexpr float kSumUnit = 1.f / (1ull << 60);  // unit of l for quantised pools
 
 // Registers of the softmax and of the other warps for quantised pools: 256 x
-// 176 + 256 x 80 = 512 x 128, what the block is launched with.
-constexpr int kSoftmaxRegs = 176, kOtherRegs = 80, kLaunchRegs = 128;
+// 168 + 256 x 88 = 512 x 128, what the block is launched with.
+constexpr int kSoftmaxRegs = 168, kOtherRegs = 88, kLaunchRegs = 128;
 
 struct TileFacts {
   int32_t bad;  // bit per 64-key block: rejected page
   float ks[2];  // K scales of the blocks' pages
-  float vs[2];  // V scales
+  float lv[2];  // log2 of the V scales
+  float iv[2];  // kSumUnit over the V scales
 };
 
 // One CTA's part of an item.
@@ -166,10 +167,23 @@ __device__ __forceinline__ GroupWork group_work(const DecodeParams& p, int g) {
   return w;
 }
 
-// First CTA whose range [c*T/C, (c+1)*T/C) reaches past step x.
-__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t C, int64_t T) {
-  return ((x + 1) * C - 1) / T;
+// a / b for a >= 0, b > 0: in 32 bits where they suffice (a 64-bit division
+// costs the start of every CTA half a microsecond).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
 }
+
+// T steps over C CTAs: the first `rest` take `each` + 1, the others `each`.
+struct Split {
+  int64_t each, rest;
+  __device__ __forceinline__ int64_t begin(int64_t c) const { return c * each + min(c, rest); }
+  // CTA whose range holds step x
+  __device__ __forceinline__ int64_t cta_of(int64_t x) const {
+    const int64_t big = rest * (each + 1);
+    return x < big ? quotient(x, each + 1) : rest + quotient(x - big, each);
+  }
+};
 
 // Position in the work list: group, head, pair of Q tiles, key tile.
 struct Cursor {
@@ -204,11 +218,11 @@ __device__ Cursor locate(const DecodeParams& p, int64_t x, int lane) {
       c.g = base + l0;
       c.w = group_work(p, c.g);
       int64_t off = x - before;
-      c.head = (int)(off / c.w.steps);
+      c.head = (int)quotient(off, c.w.steps);
       off -= c.head * c.w.steps;
-      c.pair = (int)(off / (2 * (int64_t)c.w.tiles));
+      c.pair = (int)quotient(off, 2 * (int64_t)c.w.tiles);
       off -= c.pair * 2 * (int64_t)c.w.tiles;
-      c.tile = (int)(off / pair_tiles(c.w, c.pair));
+      c.tile = (int)(pair_tiles(c.w, c.pair) == 2 ? off >> 1 : off);
       c.item_x = x - off;
       return c;
     }
@@ -248,44 +262,109 @@ __device__ int first_holder(const DecodeParams& p, const GroupWork& w, int lane)
   return -1;
 }
 
+// A landed tile of codes to f16 (exact: every E4M3 and INT8 value is one, and an
+// FP4 value times its block scale has at most 6 significant bits in [2^-10,
+// 2688]), laid out as TMA lays out 16-bit tiles.  Half h (64 rows, one page) is
+// written as zeros unless bit h of `live` is set.  A thread makes 16-byte
+// chunks of one column, eight threads a 128-byte line, so that neither its loads
+// nor its stores meet in a bank; all loads of a half come before its stores.
+template <int D, int kFmt>
+__device__ __forceinline__ void convert_codes(uint32_t src, uint32_t dst, int t, int live) {
+  constexpr int kCols = D / 8;                  // 8-value columns of a row
+  constexpr int kStep = kConvThreads / kCols;   // rows that the threads take at once
+  constexpr int kUnits = 64 / kStep;            // a thread's units of a half
+  constexpr int kRowB = row_code_bytes(kFmt, D);
+  const int col = t % kCols, r0 = t / kCols;
+  // rows kStep (8 or 16) apart have the same swizzle phase in both tiles
+  const uint32_t to = bf16_chunk<D>(dst, r0, col);
+  uint32_t from;
+  if constexpr (fp4(kFmt))
+    from = code_chunk<kRowB>(src, r0, col >> 2) + (col & 3) * 4;
+  else
+    from = code_chunk<kRowB>(src, r0, col >> 1) + (col & 1) * 8;
+  const uint32_t scales = src + kKeys * kRowB + r0 * (D / 16) + (col >> 1);  // FP4
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[kUnits][2];
+    if ((live >> h) & 1) {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int row = h * 64 + i * kStep;
+        if constexpr (fp4(kFmt)) {
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i][0]) : "r"(from + row * kRowB));
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(w[i][1]) : "r"(scales + row * (D / 16)));
+        } else {
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                       : "=r"(w[i][0]), "=r"(w[i][1])
+                       : "r"(from + row * kRowB));
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      uint32_t o[4] = {0u, 0u, 0u, 0u};
+      if ((live >> h) & 1) {
+        if constexpr (fp4(kFmt)) {
+          const uint32_t s = e4m3_splat_f16x2(w[i][1], 0);
+          e2m1x8_to_f16x2(w[i][0], o);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = hmul2_u32(o[e], s);
+        } else {
+          kv8x4_to_f16x2<kFmt>(w[i][0], o[0], o[1]);
+          kv8x4_to_f16x2<kFmt>(w[i][1], o[2], o[3]);
+        }
+      }
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + (h * 64 + i * kStep) * 128),
+                   "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                   : "memory");
+    }
+  }
+}
+
 // Row r of a bf16 Q tile (128-byte swizzled column boxes) to f16 in place, times
 // 2^e; returns e.
 template <int D>
 __device__ __forceinline__ int q_row_to_f16(uint32_t base, int r) {
-  float amax = 0.f;
+  constexpr int kBatch = 8;  // chunks in flight
+  auto load = [&](int c0, uint32_t (*w)[4]) {
 #pragma unroll
-  for (int c = 0; c < D / 8; ++c) {
-    uint32_t w[4];
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(bf16_chunk<D>(base, r, c)));
+    for (int c = 0; c < kBatch; ++c)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3])
+                   : "r"(bf16_chunk<D>(base, r, c0 + c)));
+  };
+  // the largest exponent field of a finite value: amax < 2^(top - 126)
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int c0 = 0; c0 < D / 8; c0 += kBatch) {
+    uint32_t w[kBatch][4];
+    load(c0, w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-      amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-    }
+    for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = (w[c][i] >> 7) & 0xff, hi = (w[c][i] >> 23) & 0xff;
+        top = max(top, max(lo == 0xff ? 0u : lo, hi == 0xff ? 0u : hi));
+      }
   }
-  int e = 0;
-  if (amax > 0.f && amax <= 3.4028235e38f) {
-    frexpf(amax, &e);                  // amax < 2^e
-    e = max(-114, min(100, 15 - e));   // amax * 2^e < 2^15
-  }
-  const float pre = ldexpf(1.f, e);
+  // amax * 2^e < 2^15 (zeros and subnormals, below 2^-126: e = 100)
+  const int e = min(100, 141 - (int)top);
+  const float pre = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll 1
+  for (int c0 = 0; c0 < D / 8; c0 += kBatch) {
+    uint32_t w[kBatch][4];
+    load(c0, w);
 #pragma unroll
-  for (int c = 0; c < D / 8; ++c) {
-    const uint32_t at = bf16_chunk<D>(base, r, c);
-    uint32_t w[4];
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(at));
+    for (int c = 0; c < kBatch; ++c) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-      w[i] = pack_f16(f.x * pre, f.y * pre);
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[c][i]));
+        w[c][i] = pack_f16(f.x * pre, f.y * pre);
+      }
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(bf16_chunk<D>(base, r, c0 + c)),
+                   "r"(w[c][0]), "r"(w[c][1]), "r"(w[c][2]), "r"(w[c][3])
+                   : "memory");
     }
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3])
-                 : "memory");
   }
   return e;
 }
@@ -361,6 +440,32 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
     fence_barrier_init();
   }
   if (warp == kMmaWarp) tmem_alloc(&ct.tmem, kTmemCols);
+  if (warp == kProducerWarp && lane == 0) {
+    tma_prefetch_desc(&tmap_q);
+    tma_prefetch_desc(&tmap_k);
+    tma_prefetch_desc(&tmap_v);
+  }
+  // This CTA's range of the work list and its first item, under the set-up.
+  Split split{1, 0};
+  int64_t x = 0, x_end = 0;
+  Cursor cur{};
+  int b_table = -1;
+  if (warp == kSchedWarp) {
+    bool pairs = false;
+    const int64_t T = total_steps(p, lane, &pairs);
+    // Every range holds a whole tile (two steps of an item with two Q tiles).
+    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, pairs ? T >> 1 : T));
+    split.each = quotient(T, ctas);
+    split.rest = T - split.each * ctas;
+    if (blockIdx.x < ctas) {
+      x = split.begin(blockIdx.x);
+      x_end = split.begin(blockIdx.x + 1);
+    }
+    if (x < x_end) {
+      cur = locate(p, x, lane);
+      b_table = first_holder(p, cur.w, lane);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -382,27 +487,36 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
     const uint32_t colS = col_s(x), colO = col_o(x);
     uint32_t j0 = 0, steps = 0, outs = 0;  // key tiles, steps and O tiles so far
     bool ok = true;
-    Segment sg;
-    for (uint32_t k = 0; ok && take_segment(k, &sg); ++k) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ct.seg_empty[k % kSegRing]);
+    Segment sg{};
+    // The first pass runs on whatever TMEM holds and leaves nothing behind: while
+    // the first tiles load it brings the instructions of the loop to this SM,
+    // which would cost the first real step 1.8 us.
+    sg.n = 1, sg.prefix = kKeys;
+    bool dry = true;
+    for (uint32_t k = 0; ok; k += dry ? 0 : 1, dry = false) {
+      if (!dry) {
+        if (!take_segment(k, &sg)) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ct.seg_empty[k % kSegRing]);
+      }
       const bool pairs = sg.rows > kRows;
-      const int mine = pairs ? sg.n : (sg.n + 1 - x) >> 1;  // steps of this slot
+      const int mine = pairs ? sg.n : dry ? 1 : (sg.n + 1 - x) >> 1;  // steps of this slot
       float m_ref = -INFINITY, l = 0.f;
       float row_mul = p.scale_log2;
-      if (quant(kFmt) && mine > 0) {
+      if (quant(kFmt) && mine > 0 && !dry) {
         if (!mbar_wait(&ct.qc_full, k & 1, p.flags)) { ok = false; break; }
         row_mul = ldexpf(p.scale_log2, -ct.q_exp[k & 1][pairs ? x : 0][r]);
       }
       for (int q = 0; q < mine; ++q) {
         const int i = pairs ? q : 2 * q + x;  // local key tile
         const uint32_t j = j0 + i;
-        if (!mbar_wait(&ct.s_full[x], (steps + q) & 1, p.flags) ||
-            !mbar_wait(&ct.facts_full[j % kFactsRing], (j / kFactsRing) & 1, p.flags)) {
+        if (!dry && (!mbar_wait(&ct.s_full[x], (steps + q) & 1, p.flags) ||
+                     !mbar_wait(&ct.facts_full[j % kFactsRing], (j / kFactsRing) & 1, p.flags))) {
           ok = false;
           break;
         }
-        const TileFacts tf = ct.facts[j % kFactsRing];
+        TileFacts tf = ct.facts[j % kFactsRing];
+        if (dry) tf.bad = 0;
         tc_fence_after();
         const int32_t key0 = (sg.tile0 + i) * kKeys;
         const float mul0 = quant(kFmt) ? row_mul * tf.ks[0] : row_mul;
@@ -412,12 +526,8 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         // the f16 P keeps its 11 bits whatever the scales are; the row sum takes
         // P / vs.  (m is a reference only: l and o carry the same 2^-m.)  l is
         // held 2^-60 smaller, so that it stays in range for every scale.
-        float lv0 = 0.f, lv1 = 0.f, iv0 = 1.f, iv1 = 1.f;
-        if constexpr (quant(kFmt)) {
-          const float v0 = fmaxf(tf.vs[0], kTiny), v1 = fmaxf(tf.vs[1], kTiny);
-          lv0 = log2f(v0), iv0 = kSumUnit / v0;
-          lv1 = log2f(v1), iv1 = kSumUnit / v1;
-        }
+        const float lv0 = quant(kFmt) ? tf.lv[0] : 0.f, lv1 = quant(kFmt) ? tf.lv[1] : 0.f;
+        const float iv0 = quant(kFmt) ? tf.iv[0] : 1.f, iv1 = quant(kFmt) ? tf.iv[1] : 1.f;
         // A block is live whole or not at all: pages, and with them the prefix,
         // end on 64 keys.
         const bool on0 = !(tf.bad & 1);
@@ -485,15 +595,17 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
             for (int e = 0; e < 32; ++e) pk[e] = 0u;
           }
           // P column c/2 lies in an S column already read
-          tmem_st16(tmem + lane_base + colS + cb / 2, pk);
-          tmem_st16(tmem + lane_base + colS + cb / 2 + 16, pk + 16);
+          if (!dry) {
+            tmem_st16(tmem + lane_base + colS + cb / 2, pk);
+            tmem_st16(tmem + lane_base + colS + cb / 2 + 16, pk + 16);
+          }
         }
         if (__any_sync(0xffffffffu, alpha != 1.f)) rescale_o<D>(tmem + lane_base + colO, alpha);
         l = l * alpha + rs;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ct.p_full[x]);
+        if (lane == 0 && !dry) mbar_arrive(&ct.p_full[x]);
       }
       // --------------------------------------------------------- partials
       // Rows of slot x: float4 vectors [D/4][rows of the slot], so that a warp's
@@ -507,8 +619,10 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       // (no step or no live key: l = 0; NaN passes)
       if (out_ok) sp.pre_ml[row0 + r] = make_float2(m_ref + (quant(kFmt) ? 60.f : 0.f), l);
       if (mine > 0) {
-        if (!mbar_wait(&ct.o_full[x], outs & 1, p.flags)) { ok = false; break; }
-        ++outs;
+        if (!dry) {
+          if (!mbar_wait(&ct.o_full[x], outs & 1, p.flags)) { ok = false; break; }
+          ++outs;
+        }
         tc_fence_after();
         float4* dst = reinterpret_cast<float4*>(sp.pre_o) + row0 * (D / 4) + r;
 #pragma unroll
@@ -524,19 +638,16 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           }
         }
       }
-      steps += mine;
-      j0 += sg.n;
+      if (!dry) {
+        steps += mine;
+        j0 += sg.n;
+      }
     }
   } else {
     if constexpr (quant(kFmt)) set_registers<kOtherRegs, false>();
     if (warp == kSchedWarp) {
       // ------------------------------------------------------------ scheduler
-      // This CTA's range of the work list, one descriptor per item it reaches.
-      bool pairs = false;
-      const int64_t T = total_steps(p, lane, &pairs);
-      // Every range holds a whole tile (two steps of an item with two Q tiles).
-      int64_t Ce = min((int64_t)gridDim.x, pairs ? T / 2 : T);
-      if (Ce < 1) Ce = 1;
+      // One descriptor per item that this CTA's range reaches.
       const int64_t c = blockIdx.x;
       if (c == 0)
         for (int g = lane; g < p.num_groups; g += 32) {
@@ -544,14 +655,16 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           if (b0 < 0 || b1 < b0 || b1 > p.batch || __ldg(p.prefix_lens + g) < 0)
             flag_error(p.flags, PKV_FLAG_BAD_LENGTH);
         }
-      const int64_t x_end = (c + 1) * T / Ce;
-      int64_t x = c < Ce ? c * T / Ce : x_end;
       uint32_t k = 0;
+      bool first = true;  // `cur` is the item at x
       while (true) {
         Segment s{};
         if (x < x_end) {
-          const Cursor cur = locate(p, x, lane);
-          const int b_table = first_holder(p, cur.w, lane);
+          if (!first) {
+            cur = locate(p, x, lane);
+            b_table = first_holder(p, cur.w, lane);
+          }
+          first = false;
           const int w = pair_tiles(cur.w, cur.pair);
           s.b0 = cur.w.b0 + cur.pair * 2 * TQ;
           s.b1 = min(cur.w.b1, s.b0 + 2 * TQ);
@@ -561,7 +674,8 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           s.prefix = cur.w.prefix;
           s.tile0 = cur.tile;
           // tiles whose last step lies before the range's end
-          s.n = (int)min((int64_t)cur.w.tiles, (x_end - cur.item_x) / w) - s.tile0;
+          const int64_t left = x_end - cur.item_x;
+          s.n = (int)min((int64_t)cur.w.tiles, w == 2 ? left >> 1 : left) - s.tile0;
           if (b_table < 0) s.n = 0;  // nobody to read the result
           // Items of one CTA lie 2 * rows apart, parts of an item kPairRows: no two
           // segments overlap, and the last ends by 2 * batch * heads + kPairRows * CTAs.
@@ -570,8 +684,8 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
                                     (int64_t)cur.pair * kPairRows);
           s.row_base = (int32_t)(base + (int64_t)kPairRows * c);
           if (s.tile0 == 0 && s.n > 0) {
-            const int64_t c0 = cta_of(cur.item_x + w - 1, Ce, T);
-            const int64_t c1 = cta_of(cur.item_x + (int64_t)cur.w.tiles * w - 1, Ce, T);
+            const int64_t c0 = split.cta_of(cur.item_x + w - 1);
+            const int64_t c1 = split.cta_of(cur.item_x + (int64_t)cur.w.tiles * w - 1);
             const int4 info =
                 make_int4((int)(base + kPairRows * c0), (int)(c1 - c0 + 1), s.b0, s.rows);
             for (int b = s.b0 + lane; b < s.b1; b += 32)
@@ -591,122 +705,14 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       }
     } else if (warp == kProducerWarp) {
       // ------------------------------------------------------------- producer
-      if (lane == 0) {
-        tma_prefetch_desc(&tmap_q);
-        tma_prefetch_desc(&tmap_k);
-        tma_prefetch_desc(&tmap_v);
-        const uint64_t pol = policy_evict_first();
-        // bytes of one operand (K or V) per live 64-key block
-        constexpr uint32_t kBlockBytes =
-            quant(kFmt) ? 64u * (Sm::kCodeRowB + Sm::kScaleRowB) : Sm::kHalves * 64u * 128u;
-        Ring ring;
-        uint32_t j = 0, used = 0;  // key tiles so far; slots with a fill
-        bool ok = true;
-        Segment sg;
-        for (uint32_t k = 0; ok && take_segment(k, &sg); ++k) {
-          mbar_arrive(&ct.seg_empty[k % kSegRing]);
-          const bool pairs = sg.rows > kRows;
-          const int depth = ring_depth(pairs);
-          ring.enter(depth);
-          // page lookup of tile i: page ids, scales, rejected 64-key blocks
-          struct Lookup {
-            TileFacts tf;
-            int32_t ys[2];
-            int live;
-          };
-          auto lookup = [&](int i) -> Lookup {
-            Lookup lk;
-            lk.tf.bad = 0;
-            lk.live = 0;
-            for (int sb = 0; sb < 2; ++sb) {
-              lk.tf.ks[sb] = lk.tf.vs[sb] = 1.f;
-              lk.ys[sb] = 0;
-              const int32_t key0 = (sg.tile0 + i) * kKeys + sb * 64;
-              if (key0 >= sg.prefix) continue;
-              const int32_t pid =
-                  __ldg(p.page_table + (int64_t)sg.b_table * p.max_pages + key0 / p.page_size);
-              if (pid < 0 || pid >= p.num_pages) {
-                flag_error(p.flags, PKV_FLAG_BAD_PAGE);
-                lk.tf.bad |= 1 << sb;
-                continue;
-              }
-              if constexpr (quant(kFmt)) {
-                const float ks = __ldg(p.k_scale + (int64_t)pid * p.num_kv_heads + sg.head);
-                const float vs = __ldg(p.v_scale + (int64_t)pid * p.num_kv_heads + sg.head);
-                if (!(ks > 0.f && ks <= 32768.f && vs > 0.f && vs <= 32768.f)) {
-                  flag_error(p.flags, PKV_FLAG_BAD_SCALE);
-                  lk.tf.bad |= 1 << sb;
-                  continue;
-                }
-                lk.tf.ks[sb] = ks;
-                lk.tf.vs[sb] = vs;
-              }
-              lk.ys[sb] = (int32_t)(((int64_t)pid * p.num_kv_heads + sg.head) * p.page_size +
-                                    key0 % p.page_size);
-              lk.live |= 1 << sb;
-            }
-            return lk;
-          };
-          auto load = [&](const CUtensorMap* map, const uint8_t* blocks, uint8_t* dst,
-                          uint64_t* bar, const Lookup& lk) {
-            mbar_arrive_expect_tx(bar, (uint32_t)__popc(lk.live) * kBlockBytes);
-            for (int sb = 0; sb < 2; ++sb) {
-              if (!((lk.live >> sb) & 1)) continue;
-              if constexpr (quant(kFmt)) {
-                tma_load_2d(dst + sb * 64 * Sm::kCodeRowB, map, 0, lk.ys[sb], bar, pol);
-                if constexpr (fp4(kFmt))
-                  bulk_load(dst + Sm::kCodesB + sb * 64 * Sm::kScaleRowB,
-                            blocks + (int64_t)lk.ys[sb] * Sm::kScaleRowB, 64u * Sm::kScaleRowB, bar);
-              } else {
-  #pragma unroll
-                for (int h = 0; h < Sm::kHalves; ++h)
-                  tma_load_2d(dst + h * Sm::kHalfB + sb * 64 * 128, map, h * 64, lk.ys[sb], bar,
-                              pol);
-              }
-            }
-          };
-          Lookup cur = lookup(0);
-          for (int i = 0; i < sg.n; ++i, ++j) {
-            const int st = ring.slot;
-            const uint32_t free_parity = ring.parity() ^ 1;
-            if (!mbar_wait(&ct.k_empty[st], free_parity, p.flags)) { ok = false; break; }
-            ct.facts[j % kFactsRing] = cur.tf;
-            mbar_arrive(&ct.facts_full[j % kFactsRing]);
-            load(&tmap_k, p.k_blocks, k_slot(st), &ct.k_full[st], cur);
-            if (i == 0) {  // the queries: behind the last S of the segment before
-              if (!mbar_wait(&ct.q_empty, (k & 1) ^ 1, p.flags)) {
-                ok = false;
-                mbar_wait(&ct.k_full[st], ring.parity(), p.flags);  // let the load land
-                break;
-              }
-              mbar_arrive_expect_tx(&ct.q_full, (uint32_t)(pairs ? 2 : 1) * Sm::kQB);
-              for (int x = 0; x < (pairs ? 2 : 1); ++x)
-  #pragma unroll
-                for (int h = 0; h < Sm::kHalves; ++h)
-                  tma_load_3d(sq + x * Sm::kQB + h * (kRows * 128), &tmap_q, h * 64, sg.head * G,
-                              sg.b0 + x * TQ, &ct.q_full);
-            }
-            if (!mbar_wait(&ct.v_empty[st], free_parity, p.flags)) { ok = false; break; }
-            load(&tmap_v, p.v_blocks, v_slot(st), &ct.v_full[st], cur);
-            used |= 1u << st;
-            ring.advance(depth);
-            if (i + 1 < sg.n) cur = lookup(i + 1);  // ahead of the next slot wait
-          }
-        }
-        // No copy may be on its way to this CTA's shared memory when it ends.  (One
-        // issued before a wait that gave up had that wait's whole limit to land.)
-        for (int st = 0; st <= Sm::kStages; ++st)
-          if ((used >> st) & 1) {
-            mbar_wait(&ct.k_full[st], ((ring.parities >> st) & 1) ^ 1, p.flags);
-            mbar_wait(&ct.v_full[st], ((ring.parities >> st) & 1) ^ 1, p.flags);
-          }
-      }
-    } else if (quant(kFmt) && warp >= kConvWarp0) {
-      // ------------------------------------------- codes -> f16 converters
-      const int t = threadIdx.x - kConvWarp0 * 32;
-      const uint32_t kc = smem_u32(sconv), vc = kc + Sm::kTileB;
+      // The whole warp walks the tiles, lane 0 issues.  A lane looks up one of 32
+      // consecutive 64-key blocks (16 tiles): page id, scales.
+      const uint64_t pol = policy_evict_first();
+      // bytes of one operand (K or V) per live 64-key block
+      constexpr uint32_t kBlockBytes =
+          quant(kFmt) ? 64u * (Sm::kCodeRowB + Sm::kScaleRowB) : Sm::kHalves * 64u * 128u;
       Ring ring;
-      uint32_t j = 0;
+      uint32_t j = 0, used = 0;  // key tiles so far; slots with a fill
       bool ok = true;
       Segment sg;
       for (uint32_t k = 0; ok && take_segment(k, &sg); ++k) {
@@ -715,47 +721,169 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         const bool pairs = sg.rows > kRows;
         const int depth = ring_depth(pairs);
         ring.enter(depth);
-        // Q to f16 in place, a row a thread, times the power of two that puts the
-        // row's largest value in [2^14, 2^15): bf16's 8 bits fit f16's 11, and what
-        // is small enough to lose bits is 2^-28 of the largest.
-        if (!mbar_wait(&ct.q_full, k & 1, p.flags)) break;
-        for (int x = 0; x < (pairs ? 2 : 1); ++x)
-          ct.q_exp[k & 1][x][t] = (int8_t)q_row_to_f16<D>(smem_u32(sq) + x * Sm::kQB, t);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ct.qc_full);
+        int my_bad = 0, my_live = 0;  // this lane's block: rejected page; to load
+        int32_t my_y = 0;             // its first pool row
+        float my_ks = 1.f, my_lv = 0.f, my_iv = 1.f;
+        auto lookup = [&](int i) {
+          const int32_t key0 = (sg.tile0 + i) * kKeys + lane * 64;
+          my_bad = my_live = 0;
+          if (key0 >= sg.prefix || key0 >= (sg.tile0 + sg.n) * kKeys) return;
+          const int32_t pid =
+              __ldg(p.page_table + (int64_t)sg.b_table * p.max_pages + key0 / p.page_size);
+          if (pid < 0 || pid >= p.num_pages) {
+            flag_error(p.flags, PKV_FLAG_BAD_PAGE);
+            my_bad = 1;
+            return;
+          }
+          if constexpr (quant(kFmt)) {
+            my_ks = __ldg(p.k_scale + (int64_t)pid * p.num_kv_heads + sg.head);
+            const float vs = __ldg(p.v_scale + (int64_t)pid * p.num_kv_heads + sg.head);
+            if (!(my_ks > 0.f && my_ks <= 32768.f && vs > 0.f && vs <= 32768.f)) {
+              flag_error(p.flags, PKV_FLAG_BAD_SCALE);
+              my_bad = 1;
+              return;
+            }
+            my_lv = log2f(fmaxf(vs, kTiny));
+            my_iv = kSumUnit / fmaxf(vs, kTiny);
+          }
+          my_y = (int32_t)(((int64_t)pid * p.num_kv_heads + sg.head) * p.page_size +
+                           key0 % p.page_size);
+          my_live = 1;
+        };
         for (int i = 0; i < sg.n; ++i, ++j) {
+          if ((i & 15) == 0) lookup(i);
+          TileFacts tf;
+          int32_t ys[2];
+          int live = 0;
+          tf.bad = 0;
+#pragma unroll
+          for (int sb = 0; sb < 2; ++sb) {
+            const int from = 2 * (i & 15) + sb;
+            tf.bad |= __shfl_sync(0xffffffffu, my_bad, from) << sb;
+            live |= __shfl_sync(0xffffffffu, my_live, from) << sb;
+            ys[sb] = __shfl_sync(0xffffffffu, my_y, from);
+            if constexpr (quant(kFmt)) {  // (of no meaning in blocks that are not live)
+              tf.ks[sb] = __shfl_sync(0xffffffffu, my_ks, from);
+              tf.lv[sb] = __shfl_sync(0xffffffffu, my_lv, from);
+              tf.iv[sb] = __shfl_sync(0xffffffffu, my_iv, from);
+            }
+          }
+          auto load = [&](const CUtensorMap* map, const uint8_t* blocks, uint8_t* dst,
+                          uint64_t* bar) {
+            mbar_arrive_expect_tx(bar, (uint32_t)__popc(live) * kBlockBytes);
+#pragma unroll
+            for (int sb = 0; sb < 2; ++sb) {
+              if (!((live >> sb) & 1)) continue;
+              if constexpr (quant(kFmt)) {
+                tma_load_2d(dst + sb * 64 * Sm::kCodeRowB, map, 0, ys[sb], bar, pol);
+                if constexpr (fp4(kFmt))
+                  bulk_load(dst + Sm::kCodesB + sb * 64 * Sm::kScaleRowB,
+                            blocks + (int64_t)ys[sb] * Sm::kScaleRowB, 64u * Sm::kScaleRowB, bar);
+              } else {
+#pragma unroll
+                for (int h = 0; h < Sm::kHalves; ++h)
+                  tma_load_2d(dst + h * Sm::kHalfB + sb * 64 * 128, map, h * 64, ys[sb], bar,
+                              pol);
+              }
+            }
+          };
+          const int st = ring.slot;
+          const uint32_t free_parity = ring.parity() ^ 1;
+          if (!mbar_wait(&ct.k_empty[st], free_parity, p.flags)) { ok = false; break; }
+          if (lane == 0) {
+            ct.facts[j % kFactsRing] = tf;
+            mbar_arrive(&ct.facts_full[j % kFactsRing]);
+            load(&tmap_k, p.k_blocks, k_slot(st), &ct.k_full[st]);
+          }
+          __syncwarp();
+          if (i == 0) {  // the queries: behind the last S of the segment before
+            if (!mbar_wait(&ct.q_empty, (k & 1) ^ 1, p.flags)) { ok = false; break; }
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&ct.q_full, (uint32_t)(pairs ? 2 : 1) * Sm::kQB);
+              for (int x = 0; x < (pairs ? 2 : 1); ++x)
+#pragma unroll
+                for (int h = 0; h < Sm::kHalves; ++h)
+                  tma_load_3d(sq + x * Sm::kQB + h * (kRows * 128), &tmap_q, h * 64, sg.head * G,
+                              sg.b0 + x * TQ, &ct.q_full);
+            }
+            __syncwarp();
+          }
+          if (!mbar_wait(&ct.v_empty[st], free_parity, p.flags)) { ok = false; break; }
+          if (lane == 0) load(&tmap_v, p.v_blocks, v_slot(st), &ct.v_full[st]);
+          __syncwarp();
+          used |= 1u << st;
+          ring.advance(depth);
+        }
+      }
+      // No copy may be on its way to this CTA's shared memory when it ends.  (One
+      // issued before a wait that gave up had that wait's whole limit to land.)
+      for (int st = 0; st <= Sm::kStages; ++st)
+        if ((used >> st) & 1) {
+          mbar_wait(&ct.k_full[st], ((ring.parities >> st) & 1) ^ 1, p.flags);
+          mbar_wait(&ct.v_full[st], ((ring.parities >> st) & 1) ^ 1, p.flags);
+        }
+    } else if (quant(kFmt) && warp >= kConvWarp0) {
+      // ------------------------------------------- codes -> f16 converters
+      const int t = threadIdx.x - kConvWarp0 * 32;
+      const uint32_t kc = smem_u32(sconv), vc = kc + Sm::kTileB;
+      Ring ring;
+      uint32_t j = 0;
+      bool ok = true;
+      Segment sg{};
+      sg.n = 1;
+      bool dry = true;  // as in the softmax: the first pass only fetches instructions
+      for (uint32_t k = 0; ok; k += dry ? 0 : 1, dry = false) {
+        if (!dry) {
+          if (!take_segment(k, &sg)) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ct.seg_empty[k % kSegRing]);
+        }
+        const int tiles_q = sg.rows > kRows ? 2 : 1;
+        const int depth = ring_depth(tiles_q == 2);
+        ring.enter(depth);
+        for (int i = 0; i < sg.n; ++i) {
           const int st = ring.slot;
           const uint32_t par = ring.parity();
-          if (!mbar_wait(&ct.k_full[st], par, p.flags)) { ok = false; break; }
-          const uint32_t k_codes = smem_u32(k_slot(st)), v_codes = smem_u32(v_slot(st));
-          const int bad = ct.facts[j % kFactsRing].bad;
-          const int32_t key0 = (sg.tile0 + i) * kKeys;
-          const int zero_from = min(kKeys, sg.prefix - key0);
-          if (!mbar_wait(&ct.kc_free, (j & 1) ^ 1, p.flags)) { ok = false; break; }
-          if constexpr (fp4(kFmt))
-            convert_fp4_tile<D, true, kConvThreads>(k_codes, kc, t, zero_from, bad);
-          else
-            convert_tile<D, kFmt, true, kConvThreads>(k_codes, kc, t, zero_from, bad);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ct.kc_full);
-            mbar_arrive(&ct.k_empty[st]);
+          int live = 3;
+#pragma unroll 1
+          for (int v = 0; v < 2; ++v) {  // K, then V
+            if (!dry && !mbar_wait(v ? &ct.v_full[st] : &ct.k_full[st], par, p.flags)) {
+              ok = false;
+              break;
+            }
+            // (pages, and with them the prefix, end on 64 keys)
+            if (!dry)
+              live = ~ct.facts[j % kFactsRing].bad &
+                     ((sg.tile0 + i) * kKeys + 64 < sg.prefix ? 3 : 1);
+            if (!dry && !mbar_wait(v ? &ct.vc_free : &ct.kc_free, (j & 1) ^ 1, p.flags)) {
+              ok = false;
+              break;
+            }
+            convert_codes<D, kFmt>(smem_u32(v ? v_slot(st) : k_slot(st)), v ? vc : kc, t, live);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0 && !dry) {
+              mbar_arrive(v ? &ct.vc_full : &ct.kc_full);
+              mbar_arrive(v ? &ct.v_empty[st] : &ct.k_empty[st]);
+            }
+            if (v == 0 && i == 0 && !dry) {
+              // Q to f16 in place, a row a thread, times the power of two that puts
+              // the row's largest value in [2^14, 2^15): bf16's 8 bits fit f16's 11,
+              // and what is small enough to lose bits is 2^-28 of the largest.
+              if (!mbar_wait(&ct.q_full, k & 1, p.flags)) {
+                ok = false;
+                break;
+              }
+              for (int x = 0; x < tiles_q; ++x)
+                ct.q_exp[k & 1][x][t] = (int8_t)q_row_to_f16<D>(smem_u32(sq) + x * Sm::kQB, t);
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&ct.qc_full);
+            }
           }
-          if (!mbar_wait(&ct.v_full[st], par, p.flags)) { ok = false; break; }
-          if (!mbar_wait(&ct.vc_free, (j & 1) ^ 1, p.flags)) { ok = false; break; }
-          if constexpr (fp4(kFmt))
-            convert_fp4_tile<D, true, kConvThreads>(v_codes, vc, t, zero_from, bad);
-          else
-            convert_tile<D, kFmt, true, kConvThreads>(v_codes, vc, t, zero_from, bad);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ct.vc_full);
-            mbar_arrive(&ct.v_empty[st]);
-          }
+          if (!ok || dry) break;
           ring.advance(depth);
+          ++j;
         }
       }
     } else if (warp == kMmaWarp) {
