@@ -500,6 +500,8 @@ static int decode_entry(const pkv_cache* cache, const void* q, int32_t num_q_hea
     p.cu_groups = groups->cu;
     p.prefix_lens = groups->prefix_lens;
     p.num_groups = groups->num;
+    p.num_sms = sms;
+    p.ctas_per_sm = per_sm;
     SharedParams sp{};
     sp.d = p;
     sp.own_slots = (int32_t)slots;

@@ -33,40 +33,6 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// Tokens that the sequences of group g share: sequences [cu_groups[g],
-// cu_groups[g + 1]) share their first prefix_lens[g] tokens, rounded down to
-// whole pages.  0 for a group of one sequence, whose prefix is read no more
-// often than any other token of it, and for bounds outside the batch.
-__device__ __forceinline__ int32_t group_tokens(const int32_t* cu_groups,
-                                                const int32_t* prefix_lens, int g, int batch,
-                                                int page_size, int max_pages) {
-  const int32_t b0 = __ldg(cu_groups + g), b1 = __ldg(cu_groups + g + 1);
-  if (b0 < 0 || b1 > batch || b1 - b0 < 2) return 0;
-  const int32_t pages = __ldg(prefix_lens + g) / page_size;  // < 1 for negative lengths
-  return max(0, min(pages, max_pages)) * page_size;
-}
-
-// Tokens of sequence b (of `len` tokens) that it shares with its group: 0
-// outside the groups.  A sequence that does not hold the whole prefix shares
-// nothing: all its tokens are its own, so it needs no mask in the prefix part,
-// and no value behind its end can reach it.
-__device__ __forceinline__ int32_t shared_tokens(const int32_t* cu_groups,
-                                                 const int32_t* prefix_lens, int num_groups,
-                                                 int batch, int b, int32_t len, int page_size,
-                                                 int max_pages) {
-  int lo = 0, hi = num_groups - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(cu_groups + mid) <= b)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  if (b < __ldg(cu_groups + lo) || b >= __ldg(cu_groups + lo + 1)) return 0;
-  const int32_t n = group_tokens(cu_groups, prefix_lens, lo, batch, page_size, max_pages);
-  return len >= n ? n : 0;
-}
-
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));

@@ -34,6 +34,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "groups.cuh"
 #include "kernels.h"
 
 namespace pkv {
@@ -186,15 +187,13 @@ __device__ __forceinline__ int32_t clamp_len(const DecodeParams& p, int32_t len,
 __device__ __forceinline__ int32_t own_len(const DecodeParams& p, int b, bool report) {
   const int32_t len = clamp_len(p, __ldg(p.seq_lens + b), report);
   if (!p.cu_groups) return len;
-  return len - shared_tokens(p.cu_groups, p.prefix_lens, p.num_groups, p.batch, b, len,
-                             p.page_size, p.max_pages);
+  return len - shared_tokens(p, b, len);
 }
 
 __device__ __forceinline__ int32_t page_offset(const DecodeParams& p, int b) {
   if (!p.cu_groups) return 0;
   const int32_t len = clamp_len(p, __ldg(p.seq_lens + b), false);
-  return shared_tokens(p.cu_groups, p.prefix_lens, p.num_groups, p.batch, b, len, p.page_size,
-                       p.max_pages) / p.page_size;
+  return shared_tokens(p, b, len) / p.page_size;
 }
 
 // The work list counts each unit as its tiles plus kCost virtual tiles after
@@ -381,6 +380,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     // real tile); a unit's segment count is the number of ranges that hold
     // its real tiles, and every range between its first and last holds some.
     Ce = C < T ? C : T;
+    // With shared prefixes, as many as fit the SMs that the prefix kernel leaves.
+    if (p.cu_groups && T > 0) {
+      const int sms = p.num_sms - divide_sms<D, kFmt>(p, lane).prefix_sms;
+      Ce = min(Ce, (int64_t)max(1, sms * p.ctas_per_sm));
+    }
     if (c < Ce) {
       constexpr int kCost = unit_end_cost<kFmt>();
       const TilePos s0 = locate_tile<kTile, kCost>(p, (c * T) / Ce, lane);

@@ -82,6 +82,8 @@ struct DecodeParams {
   const int32_t* cu_groups;    // [num_groups + 1]
   const int32_t* prefix_lens;  // [num_groups]
   int32_t num_groups;
+  int32_t num_sms;      // of the device, and decode CTAs that share one
+  int32_t ctas_per_sm;
   int32_t batch;
   int32_t num_q_heads;
   int32_t num_kv_heads;

@@ -38,6 +38,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "groups.cuh"
 #include "kernels.h"
 #include "tensor.cuh"
 
@@ -151,22 +152,6 @@ struct Ring {
 };
 
 // ---------------------------------------------------------------- work list
-struct GroupWork {
-  int32_t b0, b1, prefix, tiles, q_tiles;  // q_tiles of 128 rows
-  int64_t steps;                           // of one kv head
-};
-
-__device__ __forceinline__ GroupWork group_work(const DecodeParams& p, int g) {
-  GroupWork w;
-  w.b0 = __ldg(p.cu_groups + g);
-  w.b1 = __ldg(p.cu_groups + g + 1);
-  w.prefix = group_tokens(p.cu_groups, p.prefix_lens, g, p.batch, p.page_size, p.max_pages);
-  w.tiles = (w.prefix + kKeys - 1) / kKeys;
-  w.q_tiles = w.prefix > 0 ? ((w.b1 - w.b0) * p.group + kRows - 1) / kRows : 0;
-  w.steps = (int64_t)w.tiles * w.q_tiles;
-  return w;
-}
-
 // a / b for a >= 0, b > 0: in 32 bits where they suffice (a 64-bit division
 // costs the start of every CTA half a microsecond).
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
@@ -233,21 +218,6 @@ __device__ Cursor locate(const DecodeParams& p, int64_t x, int lane) {
   c.head = c.pair = c.tile = 0;
   c.item_x = run;
   return c;
-}
-
-// Steps of all items, and whether some group has two Q tiles.  Warp-wide.
-__device__ int64_t total_steps(const DecodeParams& p, int lane, bool* pairs) {
-  int64_t t = 0;
-  bool two = false;
-  for (int g = lane; g < p.num_groups; g += 32) {
-    const GroupWork w = group_work(p, g);
-    t += w.steps;
-    two |= w.q_tiles > 1;
-  }
-  *pairs = __any_sync(0xffffffffu, two);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  return t * p.num_kv_heads;
 }
 
 // First sequence of a group that holds the whole prefix, whose table row names
@@ -451,10 +421,11 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
   Cursor cur{};
   int b_table = -1;
   if (warp == kSchedWarp) {
-    bool pairs = false;
-    const int64_t T = total_steps(p, lane, &pairs);
+    const Division dv = divide_sms<D, kFmt>(p, lane);
+    const int64_t T = dv.steps;
     // Every range holds a whole tile (two steps of an item with two Q tiles).
-    const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, pairs ? T >> 1 : T));
+    const int64_t most = min((int)gridDim.x, dv.prefix_sms);
+    const int64_t ctas = max((int64_t)1, min(most, dv.pairs ? T >> 1 : T));
     split.each = quotient(T, ctas);
     split.rest = T - split.each * ctas;
     if (blockIdx.x < ctas) {
@@ -503,7 +474,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       const int mine = pairs ? sg.n : dry ? 1 : (sg.n + 1 - x) >> 1;  // steps of this slot
       float m_ref = -INFINITY, l = 0.f;
       float row_mul = p.scale_log2;
-      if (quant(kFmt) && mine > 0 && !dry) {
+      if (quant(kFmt) && !dry) {  // (every segment: a phase left out would be mistaken later)
         if (!mbar_wait(&ct.qc_full, k & 1, p.flags)) { ok = false; break; }
         row_mul = ldexpf(p.scale_log2, -ct.q_exp[k & 1][pairs ? x : 0][r]);
       }
@@ -1045,8 +1016,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   // (the arguments do not change under the kernels: read before the wait)
   const int32_t cap = p.max_pages * p.page_size;
   const int32_t len = max(0, min(__ldg(p.seq_lens + b), cap));
-  const int32_t shared = shared_tokens(p.cu_groups, p.prefix_lens, p.num_groups, p.batch, b,
-                                       len, p.page_size, p.max_pages);
+  const int32_t shared = shared_tokens(p, b, len);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // Where the parts lie (a CTA that gave up may have left its word unwritten).
