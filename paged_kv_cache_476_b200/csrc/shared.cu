@@ -95,7 +95,7 @@ struct Control {
   uint64_t k_full[kMaxStages + 1], k_empty[kMaxStages + 1];
   uint64_t v_full[kMaxStages + 1], v_empty[kMaxStages + 1];
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t kc_full, kc_free, vc_full, vc_free;  // converted tiles
+  uint64_t kc_full[2], kc_free[2], vc_full, vc_free;  // converted tiles
   uint64_t facts_full[kFactsRing];
   uint64_t done;
   TileFacts facts[kFactsRing];
@@ -121,17 +121,20 @@ struct Smem {
   static constexpr int kTileQB = kCodesB + kKeys * kScaleRowB;
   static constexpr int kOperandB = quant(kFmt) ? kTileQB : kTileB;  // K (or V) of a stage
   static constexpr int kStageB = 2 * kOperandB;
-  static constexpr int kConvB = quant(kFmt) ? 2 * kTileB : 0;  // converted K, then V
+  static constexpr int kConvB = quant(kFmt) ? 3 * kTileB : 0;  // converted K, K, V
   static constexpr int kRoom = kSmemLimit - 1024 - kControlB - 2 * kQB - kConvB;
   static constexpr int kStages = kRoom / kStageB < kMaxStages ? kRoom / kStageB : kMaxStages;
-  // An item with one Q tile leaves the other's place free: with what is left of
-  // the room it makes one stage more (K there, V in the rest), which only the
-  // two-stage ring of bf16 at D = 128 has the need of.
-  static constexpr bool kExtra = !quant(kFmt) && kStages == 2 && kQB >= kOperandB &&
-                                 kRoom - kStages * kStageB >= kOperandB;
+  // An item with one Q tile leaves the other's place free for one stage more: for
+  // quantised pools all of it, for bf16 (D = 128) its K, and V in the rest of
+  // the room.
+  static constexpr bool kExtraV = kStageB > kQB;  // V of the extra stage lies at the end
+  static constexpr bool kExtra =
+      kStages < kMaxStages && kOperandB <= kQB &&
+      (!kExtraV || kRoom - kStages * kStageB >= kOperandB);
   // (1024: the tiles' alignment)
   static constexpr int kBytes = 1024 + kControlB + 2 * kQB + kStages * kStageB + kConvB +
-                                (kExtra ? kOperandB : 0);
+                                (kExtra && kExtraV ? kOperandB : 0);
+  static_assert(kBytes <= kSmemLimit, "");
   static constexpr int kThreads = quant(kFmt) ? (kConvWarp0 + kConvWarps) * 32 : kConvWarp0 * 32;
   static_assert(kStages >= 2, "");
 };
@@ -359,14 +362,15 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
                                              ~uintptr_t(1023));
   Control& ct = *reinterpret_cast<Control*>(smem);
   uint8_t* sq = smem + kControlB;                // Q tile A, then Q tile B
-  uint8_t* sconv = sq + 2 * Sm::kQB;             // quantised: 16-bit K, then V
+  uint8_t* sconv = sq + 2 * Sm::kQB;             // quantised: 16-bit K, K, V
   uint8_t* skv = sconv + Sm::kConvB;             // stage s: K at s * kStageB, V after it
   auto k_slot = [&](int st) -> uint8_t* {
     if (Sm::kExtra && st == Sm::kStages) return sq + Sm::kQB;
     return skv + st * Sm::kStageB;
   };
   auto v_slot = [&](int st) -> uint8_t* {
-    if (Sm::kExtra && st == Sm::kStages) return skv + Sm::kStages * Sm::kStageB;
+    if (Sm::kExtra && st == Sm::kStages)
+      return Sm::kExtraV ? skv + Sm::kStages * Sm::kStageB : sq + Sm::kQB + Sm::kOperandB;
     return skv + st * Sm::kStageB + Sm::kOperandB;
   };
   auto ring_depth = [](bool pairs) { return Sm::kStages + (Sm::kExtra && !pairs ? 1 : 0); };
@@ -401,8 +405,10 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       mbar_init(&ct.p_full[x], 4);
       mbar_init(&ct.o_full[x], 1);
     }
-    mbar_init(&ct.kc_full, kConvWarps);
-    mbar_init(&ct.kc_free, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ct.kc_full[s], kConvWarps);
+      mbar_init(&ct.kc_free[s], 1);
+    }
     mbar_init(&ct.vc_full, kConvWarps);
     mbar_init(&ct.vc_free, 1);
     for (int s = 0; s < kFactsRing; ++s) mbar_init(&ct.facts_full[s], 1);
@@ -769,6 +775,14 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           __syncwarp();
           if (i == 0) {  // the queries: behind the last S of the segment before
             if (!mbar_wait(&ct.q_empty, (k & 1) ^ 1, p.flags)) { ok = false; break; }
+            if (Sm::kExtra && pairs) {  // and behind what the extra stage held in tile B's place
+              const uint32_t par = ((ring.parities >> Sm::kStages) & 1) ^ 1;
+              if (!mbar_wait(&ct.k_empty[Sm::kStages], par, p.flags) ||
+                  !mbar_wait(&ct.v_empty[Sm::kStages], par, p.flags)) {
+                ok = false;
+                break;
+              }
+            }
             if (lane == 0) {
               mbar_arrive_expect_tx(&ct.q_full, (uint32_t)(pairs ? 2 : 1) * Sm::kQB);
               for (int x = 0; x < (pairs ? 2 : 1); ++x)
@@ -796,9 +810,9 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
     } else if (quant(kFmt) && warp >= kConvWarp0) {
       // ------------------------------------------- codes -> f16 converters
       const int t = threadIdx.x - kConvWarp0 * 32;
-      const uint32_t kc = smem_u32(sconv), vc = kc + Sm::kTileB;
-      Ring ring;
-      uint32_t j = 0;
+      const uint32_t kc = smem_u32(sconv), vc = kc + 2 * Sm::kTileB;
+      Ring rings[2];            // of K and of V
+      uint32_t done[2] = {0, 0};  // key tiles converted
       bool ok = true;
       Segment sg{};
       sg.n = 1;
@@ -811,50 +825,54 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         }
         const int tiles_q = sg.rows > kRows ? 2 : 1;
         const int depth = ring_depth(tiles_q == 2);
-        ring.enter(depth);
-        for (int i = 0; i < sg.n; ++i) {
-          const int st = ring.slot;
-          const uint32_t par = ring.parity();
-          int live = 3;
+        rings[0].enter(depth);
+        rings[1].enter(depth);
+        const uint32_t first = done[0];
+        // K0, K1, V0, K2, V1, ..: a V buffer comes free late (its product waits for
+        // the softmax), so the next tile's K goes before it.
 #pragma unroll 1
-          for (int v = 0; v < 2; ++v) {  // K, then V
-            if (!dry && !mbar_wait(v ? &ct.v_full[st] : &ct.k_full[st], par, p.flags)) {
+        for (int o = 0; o < 2 * sg.n; ++o) {
+          const bool v = o == 2 * sg.n - 1 || (o > 0 && !(o & 1));
+          Ring& ring = v ? rings[1] : rings[0];
+          const uint32_t j = v ? done[1] : done[0];
+          const int st = ring.slot;
+          int live = 3;
+          if (!dry) {
+            if (!mbar_wait(v ? &ct.v_full[st] : &ct.k_full[st], ring.parity(), p.flags) ||
+                !mbar_wait(v ? &ct.vc_free : &ct.kc_free[j & 1], ((v ? j : j >> 1) & 1) ^ 1,
+                           p.flags)) {
               ok = false;
               break;
             }
             // (pages, and with them the prefix, end on 64 keys)
-            if (!dry)
-              live = ~ct.facts[j % kFactsRing].bad &
-                     ((sg.tile0 + i) * kKeys + 64 < sg.prefix ? 3 : 1);
-            if (!dry && !mbar_wait(v ? &ct.vc_free : &ct.kc_free, (j & 1) ^ 1, p.flags)) {
+            const int32_t key0 = (sg.tile0 + (int)(j - first)) * kKeys;
+            live = ~ct.facts[j % kFactsRing].bad & (key0 + 64 < sg.prefix ? 3 : 1);
+          }
+          convert_codes<D, kFmt>(smem_u32(v ? v_slot(st) : k_slot(st)),
+                                 v ? vc : kc + (j & 1) * Sm::kTileB, t, live);
+          fence_async_smem();
+          __syncwarp();
+          if (dry) continue;
+          if (lane == 0) {
+            mbar_arrive(v ? &ct.vc_full : &ct.kc_full[j & 1]);
+            mbar_arrive(v ? &ct.v_empty[st] : &ct.k_empty[st]);
+          }
+          ring.advance(depth);
+          ++(v ? done[1] : done[0]);
+          if (o == 0) {
+            // Q to f16 in place, a row a thread, times the power of two that puts
+            // the row's largest value in [2^14, 2^15): bf16's 8 bits fit f16's 11,
+            // and what is small enough to lose bits is 2^-28 of the largest.
+            if (!mbar_wait(&ct.q_full, k & 1, p.flags)) {
               ok = false;
               break;
             }
-            convert_codes<D, kFmt>(smem_u32(v ? v_slot(st) : k_slot(st)), v ? vc : kc, t, live);
+            for (int x = 0; x < tiles_q; ++x)
+              ct.q_exp[k & 1][x][t] = (int8_t)q_row_to_f16<D>(smem_u32(sq) + x * Sm::kQB, t);
             fence_async_smem();
             __syncwarp();
-            if (lane == 0 && !dry) {
-              mbar_arrive(v ? &ct.vc_full : &ct.kc_full);
-              mbar_arrive(v ? &ct.v_empty[st] : &ct.k_empty[st]);
-            }
-            if (v == 0 && i == 0 && !dry) {
-              // Q to f16 in place, a row a thread, times the power of two that puts
-              // the row's largest value in [2^14, 2^15): bf16's 8 bits fit f16's 11,
-              // and what is small enough to lose bits is 2^-28 of the largest.
-              if (!mbar_wait(&ct.q_full, k & 1, p.flags)) {
-                ok = false;
-                break;
-              }
-              for (int x = 0; x < tiles_q; ++x)
-                ct.q_exp[k & 1][x][t] = (int8_t)q_row_to_f16<D>(smem_u32(sq) + x * Sm::kQB, t);
-              fence_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&ct.qc_full);
-            }
+            if (lane == 0) mbar_arrive(&ct.qc_full);
           }
-          if (!ok || dry) break;
-          ring.advance(depth);
-          ++j;
         }
       }
     } else if (warp == kMmaWarp) {
@@ -883,8 +901,8 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         auto issue_s = [&](int s) -> bool {
           if (first_of(s)) {
             if constexpr (quant(kFmt)) {
-              k_addr = smem_u32(sconv);
-              if (!mbar_wait(&ct.kc_full, jk & 1, p.flags)) return false;
+              k_addr = smem_u32(sconv) + (jk & 1) * Sm::kTileB;
+              if (!mbar_wait(&ct.kc_full[jk & 1], (jk >> 1) & 1, p.flags)) return false;
             } else {
               k_addr = smem_u32(k_slot(kring.slot));
               if (!mbar_wait(&ct.k_full[kring.slot], kring.parity(), p.flags)) return false;
@@ -893,16 +911,17 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           const int x = s & 1;
           tc_fence_after();
           if (lane == 0) {
-            const uint32_t qa = q_addr + (pairs ? x * Sm::kQB : 0);
-  #pragma unroll
+            // (the descriptors' low bits are the address in 16-byte units)
+            const uint64_t ad = sdesc(q_addr + (pairs ? x * Sm::kQB : 0), 16, 1024);
+            const uint64_t bd = sdesc(k_addr, 16, 1024);
+#pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const int h = kk >> 2, w = kk & 3;
-              const uint64_t ad = sdesc(qa + h * (kRows * 128) + w * 32, 16, 1024);
-              const uint64_t bd = sdesc(k_addr + h * Sm::kHalfB + w * 32, 16, 1024);
-              mma_ss(tmem + col_s(x), ad, bd, id_s, kk > 0 ? 1u : 0u);
+              mma_ss(tmem + col_s(x), ad + ((h * (kRows * 128) + w * 32) >> 4),
+                     bd + ((h * Sm::kHalfB + w * 32) >> 4), id_s, kk > 0 ? 1u : 0u);
             }
             tc_commit(&ct.s_full[x]);
-            if (last_of(s)) tc_commit(quant(kFmt) ? &ct.kc_free : &ct.k_empty[kring.slot]);
+            if (last_of(s)) tc_commit(quant(kFmt) ? &ct.kc_free[jk & 1] : &ct.k_empty[kring.slot]);
             if (s == nsteps - 1) tc_commit(&ct.q_empty);
           }
           __syncwarp();
@@ -916,7 +935,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         auto issue_pv = [&](int s) -> bool {
           if (first_of(s)) {
             if constexpr (quant(kFmt)) {
-              v_addr = smem_u32(sconv) + Sm::kTileB;
+              v_addr = smem_u32(sconv) + 2 * Sm::kTileB;
               if (!mbar_wait(&ct.vc_full, jv & 1, p.flags)) return false;
             } else {
               if (!mbar_wait(&ct.v_full[vring.slot], vring.parity(), p.flags)) return false;
@@ -943,12 +962,11 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           if (!mbar_wait(&ct.p_full[x], (steps[x] + (s >> 1)) & 1, p.flags)) return false;
           tc_fence_after();
           if (lane == 0) {
-  #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk) {
-              const uint64_t bd = sdesc(v_addr + kk * 2048, Sm::kHalfB, 1024);
-              mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, bd, id_o,
+            const uint64_t bd = sdesc(v_addr, Sm::kHalfB, 1024);
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, bd + (kk * 2048 >> 4), id_o,
                      (s >= 2 || kk > 0) ? 1u : 0u);
-            }
             if (last_of(s)) tc_commit(quant(kFmt) ? &ct.vc_free : &ct.v_empty[vring.slot]);
             if (s + 2 >= nsteps) tc_commit(&ct.o_full[x]);  // the slot's last step
           }
