@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       const uint32_t q_addr = smem_u32(sq);
       Ring kring, vring;        // bf16: slots of the next K and V tile
       uint32_t jk = 0, jv = 0;  // key tiles so far, as S and as PV sees them
-      uint32_t steps[2] = {0, 0};  // of each slot, before this segment
+      uint32_t steps0 = 0, steps1 = 0;  // of each slot, before this segment
       uint32_t k_addr = 0, v_addr = 0;
       bool ok = true;
       Segment sg;
@@ -910,7 +910,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           }
           const int x = s & 1;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             // (the descriptors' low bits are the address in 16-byte units)
             const uint64_t ad = sdesc(q_addr + (pairs ? x * Sm::kQB : 0), 16, 1024);
             const uint64_t bd = sdesc(k_addr, 16, 1024);
@@ -959,9 +959,9 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
             }
           }
           const int x = s & 1;
-          if (!mbar_wait(&ct.p_full[x], (steps[x] + (s >> 1)) & 1, p.flags)) return false;
+          if (!mbar_wait(&ct.p_full[x], ((x ? steps1 : steps0) + (s >> 1)) & 1, p.flags)) return false;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             const uint64_t bd = sdesc(v_addr, Sm::kHalfB, 1024);
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
@@ -987,8 +987,8 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           if (!(ok = issue_pv(s))) break;
           if (s + 2 < nsteps) ok = issue_s(s + 2);
         }
-        steps[0] += (nsteps + 1) >> 1;
-        steps[1] += nsteps >> 1;
+        steps0 += (nsteps + 1) >> 1;
+        steps1 += nsteps >> 1;
       }
       // every MMA this thread issued must finish before TMEM is released
       if (lane == 0) tc_commit(&ct.done);

@@ -19,6 +19,16 @@ __device__ __forceinline__ uint32_t col_s(int x) { return x ? 128u : 0u; }
 __device__ __forceinline__ uint32_t col_o(int x) { return x ? 384u : 256u; }
 
 // --------------------------------------------------------- tcgen05 helpers
+// True in one lane of the (converged) warp.  Products issued under this, and
+// not under lane == 0, let the compiler see that one thread alone gives their
+// operands, which a warp takes from uniform registers (prefix kernel: 10 %).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one = 0;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t@p mov.s32 %0, 1;\n\t}"
+      : "+r"(one));
+  return one != 0;
+}
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                    smem_u32(dst_smem)),
