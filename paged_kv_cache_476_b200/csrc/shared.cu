@@ -54,7 +54,7 @@ constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kSchedWarp = 10;  // warp 11 has no role
 constexpr int kConvWarp0 = 12;
-constexpr int kConvWarps = 4;
+constexpr int kConvWarps = 4;  // for K, and as many for V
 constexpr int kConvThreads = kConvWarps * 32;
 constexpr int kSegRing = 2;  // segment descriptors ahead
 // A facts slot is refilled when the K ring has let go of a tile (at most
@@ -66,9 +66,11 @@ constexpr int kMaxSegments = 1 << 16;     // more than any GPU has SMs
 constexpr float kTiny = 1.17549435e-38f;       // smallest normal fp32
 constexpr float kSumUnit = 1.f / (1ull << 60);  // unit of l for quantised pools
 
-// Registers of the softmax and of the other warps for quantised pools: 256 x
-// 168 + 256 x 88 = 512 x 128, what the block is launched with.
-constexpr int kSoftmaxRegs = 168, kOtherRegs = 88, kLaunchRegs = 128;
+// Registers of the softmax, the load / product / scheduler and the converter
+// warps for quantised pools: 256 x 152 + 128 x 80 + 256 x 48 = 640 x 96, what
+// the block is launched with.
+constexpr int kSoftmaxRegs = 152, kIssueRegs = 80, kConvRegs = 48, kLaunchRegs = 96;
+static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs + 256 * kConvRegs <= 640 * kLaunchRegs, "");
 
 struct TileFacts {
   int32_t bad;  // bit per 64-key block: rejected page
@@ -95,7 +97,7 @@ struct Control {
   uint64_t k_full[kMaxStages + 1], k_empty[kMaxStages + 1];
   uint64_t v_full[kMaxStages + 1], v_empty[kMaxStages + 1];
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t kc_full[2], kc_free[2], vc_full, vc_free;  // converted tiles
+  uint64_t kc_full[2], kc_free[2], vc_full[1], vc_free[1];  // converted tiles
   uint64_t facts_full[kFactsRing];
   uint64_t done;
   TileFacts facts[kFactsRing];
@@ -135,7 +137,7 @@ struct Smem {
   static constexpr int kBytes = 1024 + kControlB + 2 * kQB + kStages * kStageB + kConvB +
                                 (kExtra && kExtraV ? kOperandB : 0);
   static_assert(kBytes <= kSmemLimit, "");
-  static constexpr int kThreads = quant(kFmt) ? (kConvWarp0 + kConvWarps) * 32 : kConvWarp0 * 32;
+  static constexpr int kThreads = (kConvWarp0 + (quant(kFmt) ? 2 * kConvWarps : 0)) * 32;
   static_assert(kStages >= 2, "");
 };
 
@@ -245,7 +247,7 @@ template <int D, int kFmt>
 __device__ __forceinline__ void convert_codes(uint32_t src, uint32_t dst, int t, int live) {
   constexpr int kCols = D / 8;                  // 8-value columns of a row
   constexpr int kStep = kConvThreads / kCols;   // rows that the threads take at once
-  constexpr int kUnits = 64 / kStep;            // a thread's units of a half
+  constexpr int kUnits = 4;                     // a thread's units in flight
   constexpr int kRowB = row_code_bytes(kFmt, D);
   const int col = t % kCols, r0 = t / kCols;
   // rows kStep (8 or 16) apart have the same swizzle phase in both tiles
@@ -257,12 +259,13 @@ __device__ __forceinline__ void convert_codes(uint32_t src, uint32_t dst, int t,
     from = code_chunk<kRowB>(src, r0, col >> 1) + (col & 1) * 8;
   const uint32_t scales = src + kKeys * kRowB + r0 * (D / 16) + (col >> 1);  // FP4
 #pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
+  for (int row0 = 0; row0 < kKeys; row0 += kUnits * kStep) {
+    const bool on = (live >> (row0 >> 6)) & 1;
     uint32_t w[kUnits][2];
-    if ((live >> h) & 1) {
+    if (on) {
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
-        const int row = h * 64 + i * kStep;
+        const int row = row0 + i * kStep;
         if constexpr (fp4(kFmt)) {
           asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i][0]) : "r"(from + row * kRowB));
           asm volatile("ld.shared.u8 %0, [%1];" : "=r"(w[i][1]) : "r"(scales + row * (D / 16)));
@@ -276,7 +279,7 @@ __device__ __forceinline__ void convert_codes(uint32_t src, uint32_t dst, int t,
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       uint32_t o[4] = {0u, 0u, 0u, 0u};
-      if ((live >> h) & 1) {
+      if (on) {
         if constexpr (fp4(kFmt)) {
           const uint32_t s = e4m3_splat_f16x2(w[i][1], 0);
           e2m1x8_to_f16x2(w[i][0], o);
@@ -287,7 +290,7 @@ __device__ __forceinline__ void convert_codes(uint32_t src, uint32_t dst, int t,
           kv8x4_to_f16x2<kFmt>(w[i][1], o[2], o[3]);
         }
       }
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + (h * 64 + i * kStep) * 128),
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + (row0 + i * kStep) * 128),
                    "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                    : "memory");
     }
@@ -295,10 +298,10 @@ __device__ __forceinline__ void convert_codes(uint32_t src, uint32_t dst, int t,
 }
 
 // Row r of a bf16 Q tile (128-byte swizzled column boxes) to f16 in place, times
-// 2^e; returns e.
+// 2^e (not stored unless `store`); returns e.
 template <int D>
-__device__ __forceinline__ int q_row_to_f16(uint32_t base, int r) {
-  constexpr int kBatch = 8;  // chunks in flight
+__device__ __forceinline__ int q_row_to_f16(uint32_t base, int r, bool store) {
+  constexpr int kBatch = 4;  // chunks in flight
   auto load = [&](int c0, uint32_t (*w)[4]) {
 #pragma unroll
     for (int c = 0; c < kBatch; ++c)
@@ -334,9 +337,11 @@ __device__ __forceinline__ int q_row_to_f16(uint32_t base, int r) {
         const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[c][i]));
         w[c][i] = pack_f16(f.x * pre, f.y * pre);
       }
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(bf16_chunk<D>(base, r, c0 + c)),
-                   "r"(w[c][0]), "r"(w[c][1]), "r"(w[c][2]), "r"(w[c][3])
-                   : "memory");
+      if (store)
+        asm volatile(
+            "st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(bf16_chunk<D>(base, r, c0 + c)),
+            "r"(w[c][0]), "r"(w[c][1]), "r"(w[c][2]), "r"(w[c][3])
+            : "memory");
     }
   }
   return e;
@@ -388,7 +393,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
     for (int s = 0; s < kSegRing; ++s) {
       mbar_init(&ct.seg_full[s], 1);
       // producer, MMA, softmax warps, converters
-      mbar_init(&ct.seg_empty[s], 2 + 8 + (quant(kFmt) ? kConvWarps : 0));
+      mbar_init(&ct.seg_empty[s], 2 + 8 + (quant(kFmt) ? 2 * kConvWarps : 0));
     }
     mbar_init(&ct.q_full, 1);
     mbar_init(&ct.q_empty, 1);
@@ -409,8 +414,8 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       mbar_init(&ct.kc_full[s], kConvWarps);
       mbar_init(&ct.kc_free[s], 1);
     }
-    mbar_init(&ct.vc_full, kConvWarps);
-    mbar_init(&ct.vc_free, 1);
+    mbar_init(&ct.vc_full[0], kConvWarps);
+    mbar_init(&ct.vc_free[0], 1);
     for (int s = 0; s < kFactsRing; ++s) mbar_init(&ct.facts_full[s], 1);
     mbar_init(&ct.done, 1);
     fence_barrier_init();
@@ -620,8 +625,8 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         j0 += sg.n;
       }
     }
-  } else {
-    if constexpr (quant(kFmt)) set_registers<kOtherRegs, false>();
+  } else if (warp < kConvWarp0) {
+    if constexpr (quant(kFmt)) set_registers<kIssueRegs, false>();
     if (warp == kSchedWarp) {
       // ------------------------------------------------------------ scheduler
       // One descriptor per item that this CTA's range reaches.
@@ -807,74 +812,6 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           mbar_wait(&ct.k_full[st], ((ring.parities >> st) & 1) ^ 1, p.flags);
           mbar_wait(&ct.v_full[st], ((ring.parities >> st) & 1) ^ 1, p.flags);
         }
-    } else if (quant(kFmt) && warp >= kConvWarp0) {
-      // ------------------------------------------- codes -> f16 converters
-      const int t = threadIdx.x - kConvWarp0 * 32;
-      const uint32_t kc = smem_u32(sconv), vc = kc + 2 * Sm::kTileB;
-      Ring rings[2];            // of K and of V
-      uint32_t done[2] = {0, 0};  // key tiles converted
-      bool ok = true;
-      Segment sg{};
-      sg.n = 1;
-      bool dry = true;  // as in the softmax: the first pass only fetches instructions
-      for (uint32_t k = 0; ok; k += dry ? 0 : 1, dry = false) {
-        if (!dry) {
-          if (!take_segment(k, &sg)) break;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ct.seg_empty[k % kSegRing]);
-        }
-        const int tiles_q = sg.rows > kRows ? 2 : 1;
-        const int depth = ring_depth(tiles_q == 2);
-        rings[0].enter(depth);
-        rings[1].enter(depth);
-        const uint32_t first = done[0];
-        // K0, K1, V0, K2, V1, ..: a V buffer comes free late (its product waits for
-        // the softmax), so the next tile's K goes before it.
-#pragma unroll 1
-        for (int o = 0; o < 2 * sg.n; ++o) {
-          const bool v = o == 2 * sg.n - 1 || (o > 0 && !(o & 1));
-          Ring& ring = v ? rings[1] : rings[0];
-          const uint32_t j = v ? done[1] : done[0];
-          const int st = ring.slot;
-          int live = 3;
-          if (!dry) {
-            if (!mbar_wait(v ? &ct.v_full[st] : &ct.k_full[st], ring.parity(), p.flags) ||
-                !mbar_wait(v ? &ct.vc_free : &ct.kc_free[j & 1], ((v ? j : j >> 1) & 1) ^ 1,
-                           p.flags)) {
-              ok = false;
-              break;
-            }
-            // (pages, and with them the prefix, end on 64 keys)
-            const int32_t key0 = (sg.tile0 + (int)(j - first)) * kKeys;
-            live = ~ct.facts[j % kFactsRing].bad & (key0 + 64 < sg.prefix ? 3 : 1);
-          }
-          convert_codes<D, kFmt>(smem_u32(v ? v_slot(st) : k_slot(st)),
-                                 v ? vc : kc + (j & 1) * Sm::kTileB, t, live);
-          fence_async_smem();
-          __syncwarp();
-          if (dry) continue;
-          if (lane == 0) {
-            mbar_arrive(v ? &ct.vc_full : &ct.kc_full[j & 1]);
-            mbar_arrive(v ? &ct.v_empty[st] : &ct.k_empty[st]);
-          }
-          ring.advance(depth);
-          ++(v ? done[1] : done[0]);
-          if (o == 0) {
-            // Q to f16 in place, a row a thread, times the power of two that puts
-            // the row's largest value in [2^14, 2^15): bf16's 8 bits fit f16's 11,
-            // and what is small enough to lose bits is 2^-28 of the largest.
-            if (!mbar_wait(&ct.q_full, k & 1, p.flags)) {
-              ok = false;
-              break;
-            }
-            for (int x = 0; x < tiles_q; ++x)
-              ct.q_exp[k & 1][x][t] = (int8_t)q_row_to_f16<D>(smem_u32(sq) + x * Sm::kQB, t);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ct.qc_full);
-          }
-        }
-      }
     } else if (warp == kMmaWarp) {
       // ----------------------------------------------------------------- MMA
       const uint32_t id_s = idesc_f16kind(kRows, kKeys, 0, !quant(kFmt));
@@ -936,7 +873,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           if (first_of(s)) {
             if constexpr (quant(kFmt)) {
               v_addr = smem_u32(sconv) + 2 * Sm::kTileB;
-              if (!mbar_wait(&ct.vc_full, jv & 1, p.flags)) return false;
+              if (!mbar_wait(&ct.vc_full[0], jv & 1, p.flags)) return false;
             } else {
               if (!mbar_wait(&ct.v_full[vring.slot], vring.parity(), p.flags)) return false;
               const int32_t key0 = (sg.tile0 + (pairs ? s >> 1 : s)) * kKeys;
@@ -967,7 +904,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
             for (int kk = 0; kk < kKeys / 16; ++kk)
               mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, bd + (kk * 2048 >> 4), id_o,
                      (s >= 2 || kk > 0) ? 1u : 0u);
-            if (last_of(s)) tc_commit(quant(kFmt) ? &ct.vc_free : &ct.v_empty[vring.slot]);
+            if (last_of(s)) tc_commit(quant(kFmt) ? &ct.vc_free[0] : &ct.v_empty[vring.slot]);
             if (s + 2 >= nsteps) tc_commit(&ct.o_full[x]);  // the slot's last step
           }
           __syncwarp();
@@ -993,6 +930,74 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       // every MMA this thread issued must finish before TMEM is released
       if (lane == 0) tc_commit(&ct.done);
       __syncwarp();
+    }
+  } else if constexpr (quant(kFmt)) {
+    set_registers<kConvRegs, false>();
+    // ------------------------------------------- codes -> f16 converters
+    // One warpgroup converts K, the other V and, at a segment's start, Q.
+    const bool v = warp >= kConvWarp0 + kConvWarps;
+    const int t = threadIdx.x & (kConvThreads - 1);
+    const uint32_t to = smem_u32(sconv) + (v ? 2 * Sm::kTileB : 0);
+    uint64_t* const full = v ? ct.v_full : ct.k_full;
+    uint64_t* const empty = v ? ct.v_empty : ct.k_empty;
+    uint64_t* const made = v ? ct.vc_full : ct.kc_full;
+    uint64_t* const free = v ? ct.vc_free : ct.kc_free;
+    const uint32_t buffers = v ? 1 : 2;
+    Ring ring;
+    uint32_t j = 0, buf = 0, use = 0;  // key tiles so far; buffer and its use's parity
+    bool ok = true;
+    Segment sg{};
+    sg.n = 1;
+    bool dry = true;  // as in the softmax: the first pass only fetches instructions
+    for (uint32_t k = 0; ok; k += dry ? 0 : 1, dry = false) {
+      if (!dry) {
+        if (!take_segment(k, &sg)) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ct.seg_empty[k % kSegRing]);
+      }
+      const int tiles_q = sg.rows > kRows ? 2 : 1;
+      const int depth = ring_depth(tiles_q == 2);
+      ring.enter(depth);
+      if (v) {
+        // Q to f16 in place, a row a thread, times the power of two that puts the
+        // row's largest value in [2^14, 2^15): bf16's 8 bits fit f16's 11, and what
+        // is small enough to lose bits is 2^-28 of the largest.
+        if (!dry && !mbar_wait(&ct.q_full, k & 1, p.flags)) break;
+        for (int x = 0; x < tiles_q; ++x) {
+          const int e = q_row_to_f16<D>(smem_u32(sq) + x * Sm::kQB, t, !dry);
+          if (!dry) ct.q_exp[k & 1][x][t] = (int8_t)e;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && !dry) mbar_arrive(&ct.qc_full);
+      }
+#pragma unroll 1
+      for (int i = 0; i < sg.n; ++i) {
+        const int st = ring.slot;
+        int live = 3;
+        if (!dry) {
+          if (!mbar_wait(&full[st], ring.parity(), p.flags) ||
+              !mbar_wait(&free[buf], use ^ 1, p.flags)) {
+            ok = false;
+            break;
+          }
+          // (pages, and with them the prefix, end on 64 keys)
+          live = ~ct.facts[j % kFactsRing].bad &
+                 ((sg.tile0 + i) * kKeys + 64 < sg.prefix ? 3 : 1);
+        }
+        convert_codes<D, kFmt>(smem_u32(v ? v_slot(st) : k_slot(st)), to + buf * Sm::kTileB, t,
+                               live);
+        fence_async_smem();
+        __syncwarp();
+        if (dry) break;
+        if (lane == 0) {
+          mbar_arrive(&made[buf]);
+          mbar_arrive(&empty[st]);
+        }
+        ring.advance(depth);
+        ++j;
+        if (++buf == buffers) buf = 0, use ^= 1;
+      }
     }
   }
 
