@@ -97,7 +97,7 @@ struct Control {
   uint64_t k_full[kMaxStages + 1], k_empty[kMaxStages + 1];
   uint64_t v_full[kMaxStages + 1], v_empty[kMaxStages + 1];
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t kc_full[2], kc_free[2], vc_full[1], vc_free[1];  // converted tiles
+  uint64_t kc_full[2], kc_free[2], vc_full[2], vc_free[2];  // converted tiles
   uint64_t facts_full[kFactsRing];
   uint64_t done;
   TileFacts facts[kFactsRing];
@@ -126,16 +126,14 @@ struct Smem {
   static constexpr int kConvB = quant(kFmt) ? 3 * kTileB : 0;  // converted K, K, V
   static constexpr int kRoom = kSmemLimit - 1024 - kControlB - 2 * kQB - kConvB;
   static constexpr int kStages = kRoom / kStageB < kMaxStages ? kRoom / kStageB : kMaxStages;
-  // An item with one Q tile leaves the other's place free for one stage more: for
-  // quantised pools all of it, for bf16 (D = 128) its K, and V in the rest of
-  // the room.
-  static constexpr bool kExtraV = kStageB > kQB;  // V of the extra stage lies at the end
-  static constexpr bool kExtra =
-      kStages < kMaxStages && kOperandB <= kQB &&
-      (!kExtraV || kRoom - kStages * kStageB >= kOperandB);
+  // An item with one Q tile leaves the other's place free.  Quantised pools use
+  // it for a second converted V; bf16 at D = 128 for the K of a third stage, whose
+  // V takes the rest of the room.
+  static constexpr bool kExtra = !quant(kFmt) && kStages == 2 && kOperandB <= kQB &&
+                                 kRoom - kStages * kStageB >= kOperandB;
   // (1024: the tiles' alignment)
   static constexpr int kBytes = 1024 + kControlB + 2 * kQB + kStages * kStageB + kConvB +
-                                (kExtra && kExtraV ? kOperandB : 0);
+                                (kExtra ? kOperandB : 0);
   static_assert(kBytes <= kSmemLimit, "");
   static constexpr int kThreads = (kConvWarp0 + (quant(kFmt) ? 2 * kConvWarps : 0)) * 32;
   static_assert(kStages >= 2, "");
@@ -159,9 +157,11 @@ struct Ring {
 // ---------------------------------------------------------------- work list
 // a / b for a >= 0, b > 0: in 32 bits where they suffice (a 64-bit division
 // costs the start of every CTA half a microsecond).
+__device__ __noinline__ int64_t long_quotient(int64_t a, int64_t b) { return a / b; }
+
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
+  return long_quotient(a, b);
 }
 
 // T steps over C CTAs: the first `rest` take `each` + 1, the others `each`.
@@ -297,54 +297,49 @@ __device__ __forceinline__ void convert_codes(uint32_t src, uint32_t dst, int t,
   }
 }
 
-// Row r of a bf16 Q tile (128-byte swizzled column boxes) to f16 in place, times
-// 2^e (not stored unless `store`); returns e.
+// `rows` rows of a bf16 Q tile (128-byte swizzled column boxes) to f16 in place,
+// row r times 2^q_exp[r], the power of two that puts its largest value in [2^14,
+// 2^15): bf16's 8 bits fit f16's 11, and what is small enough to lose bits is
+// 2^-28 of the largest.  Four threads share a row.
 template <int D>
-__device__ __forceinline__ int q_row_to_f16(uint32_t base, int r, bool store) {
-  constexpr int kBatch = 4;  // chunks in flight
-  auto load = [&](int c0, uint32_t (*w)[4]) {
+__device__ __forceinline__ void q_rows_to_f16(uint32_t base, int t, int rows, int8_t* q_exp,
+                                              bool store) {
+  constexpr int kChunks = D / 32;  // 16-byte chunks of a thread
+#pragma unroll 1
+  for (int r = t >> 2; r < ((rows + 7) & ~7); r += kConvThreads / 4) {  // whole warps
+    uint32_t w[kChunks][4];
 #pragma unroll
-    for (int c = 0; c < kBatch; ++c)
+    for (int c = 0; c < kChunks; ++c)
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3])
-                   : "r"(bf16_chunk<D>(base, r, c0 + c)));
-  };
-  // the largest exponent field of a finite value: amax < 2^(top - 126)
-  uint32_t top = 0;
-#pragma unroll 1
-  for (int c0 = 0; c0 < D / 8; c0 += kBatch) {
-    uint32_t w[kBatch][4];
-    load(c0, w);
+                   : "r"(bf16_chunk<D>(base, r, 4 * c + (t & 3))));
+    __nv_bfloat162 top = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
-    for (int c = 0; c < kBatch; ++c)
+    for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = (w[c][i] >> 7) & 0xff, hi = (w[c][i] >> 23) & 0xff;
-        top = max(top, max(lo == 0xff ? 0u : lo, hi == 0xff ? 0u : hi));
-      }
-  }
-  // amax * 2^e < 2^15 (zeros and subnormals, below 2^-126: e = 100)
-  const int e = min(100, 141 - (int)top);
-  const float pre = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll 1
-  for (int c0 = 0; c0 < D / 8; c0 += kBatch) {
-    uint32_t w[kBatch][4];
-    load(c0, w);
+      for (int i = 0; i < 4; ++i)  // (drops NaN)
+        top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[c][i])));
+    uint32_t amax = __float_as_uint(fmaxf(__low2float(top), __high2float(top)));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // amax < 2^(field - 126); zeros and subnormals: 2^100
+    const int e = min(100, 141 - (int)(amax >> 23));
+    const float pre = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-    for (int c = 0; c < kBatch; ++c) {
+    for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[c][i]));
         w[c][i] = pack_f16(f.x * pre, f.y * pre);
       }
       if (store)
-        asm volatile(
-            "st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(bf16_chunk<D>(base, r, c0 + c)),
-            "r"(w[c][0]), "r"(w[c][1]), "r"(w[c][2]), "r"(w[c][3])
-            : "memory");
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         bf16_chunk<D>(base, r, 4 * c + (t & 3))),
+                     "r"(w[c][0]), "r"(w[c][1]), "r"(w[c][2]), "r"(w[c][3])
+                     : "memory");
     }
+    if (store && (t & 3) == 0) q_exp[r] = (int8_t)e;
   }
-  return e;
 }
 
 template <int kRegs, bool kMore>
@@ -375,10 +370,13 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
   };
   auto v_slot = [&](int st) -> uint8_t* {
     if (Sm::kExtra && st == Sm::kStages)
-      return Sm::kExtraV ? skv + Sm::kStages * Sm::kStageB : sq + Sm::kQB + Sm::kOperandB;
+      return skv + Sm::kStages * Sm::kStageB;
     return skv + st * Sm::kStageB + Sm::kOperandB;
   };
   auto ring_depth = [](bool pairs) { return Sm::kStages + (Sm::kExtra && !pairs ? 1 : 0); };
+  // converted V tiles: the second lies in Q tile B's place
+  auto v_made = [&](int buf) -> uint8_t* { return buf ? sq + Sm::kQB : sconv + 2 * Sm::kTileB; };
+  auto v_buffers = [](bool pairs) { return pairs ? 1 : 2; };
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -413,9 +411,9 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ct.kc_full[s], kConvWarps);
       mbar_init(&ct.kc_free[s], 1);
+      mbar_init(&ct.vc_full[s], kConvWarps);
+      mbar_init(&ct.vc_free[s], 1);
     }
-    mbar_init(&ct.vc_full[0], kConvWarps);
-    mbar_init(&ct.vc_free[0], 1);
     for (int s = 0; s < kFactsRing; ++s) mbar_init(&ct.facts_full[s], 1);
     mbar_init(&ct.done, 1);
     fence_barrier_init();
@@ -473,8 +471,9 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
     // The first pass runs on whatever TMEM holds and leaves nothing behind: while
     // the first tiles load it brings the instructions of the loop to this SM,
     // which would cost the first real step 1.8 us.
-    sg.n = 1, sg.prefix = kKeys;
-    bool dry = true;
+    bool dry = take_segment(0, &sg);
+    ok = dry;
+    sg.rows = 0, sg.n = 1, sg.tile0 = 0, sg.prefix = kKeys;
     for (uint32_t k = 0; ok; k += dry ? 0 : 1, dry = false) {
       if (!dry) {
         if (!take_segment(k, &sg)) break;
@@ -631,12 +630,6 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       // ------------------------------------------------------------ scheduler
       // One descriptor per item that this CTA's range reaches.
       const int64_t c = blockIdx.x;
-      if (c == 0)
-        for (int g = lane; g < p.num_groups; g += 32) {
-          const int32_t b0 = __ldg(p.cu_groups + g), b1 = __ldg(p.cu_groups + g + 1);
-          if (b0 < 0 || b1 < b0 || b1 > p.batch || __ldg(p.prefix_lens + g) < 0)
-            flag_error(p.flags, PKV_FLAG_BAD_LENGTH);
-        }
       uint32_t k = 0;
       bool first = true;  // `cur` is the item at x
       while (true) {
@@ -685,6 +678,12 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         ++k;
         if (s.n == 0) break;
       }
+      if (c == 0)
+        for (int g = lane; g < p.num_groups; g += 32) {
+          const int32_t b0 = __ldg(p.cu_groups + g), b1 = __ldg(p.cu_groups + g + 1);
+          if (b0 < 0 || b1 < b0 || b1 > p.batch || __ldg(p.prefix_lens + g) < 0)
+            flag_error(p.flags, PKV_FLAG_BAD_LENGTH);
+        }
     } else if (warp == kProducerWarp) {
       // ------------------------------------------------------------- producer
       // The whole warp walks the tiles, lane 0 issues.  A lane looks up one of 32
@@ -694,6 +693,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       constexpr uint32_t kBlockBytes =
           quant(kFmt) ? 64u * (Sm::kCodeRowB + Sm::kScaleRowB) : Sm::kHalves * 64u * 128u;
       Ring ring;
+      Ring v_ring;               // (quantised) as the converters walk V's buffers
       uint32_t j = 0, used = 0;  // key tiles so far; slots with a fill
       bool ok = true;
       Segment sg;
@@ -703,6 +703,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         const bool pairs = sg.rows > kRows;
         const int depth = ring_depth(pairs);
         ring.enter(depth);
+        v_ring.enter(v_buffers(pairs));
         int my_bad = 0, my_live = 0;  // this lane's block: rejected page; to load
         int32_t my_y = 0;             // its first pool row
         float my_ks = 1.f, my_lv = 0.f, my_iv = 1.f;
@@ -780,13 +781,12 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           __syncwarp();
           if (i == 0) {  // the queries: behind the last S of the segment before
             if (!mbar_wait(&ct.q_empty, (k & 1) ^ 1, p.flags)) { ok = false; break; }
-            if (Sm::kExtra && pairs) {  // and behind what the extra stage held in tile B's place
-              const uint32_t par = ((ring.parities >> Sm::kStages) & 1) ^ 1;
-              if (!mbar_wait(&ct.k_empty[Sm::kStages], par, p.flags) ||
-                  !mbar_wait(&ct.v_empty[Sm::kStages], par, p.flags)) {
-                ok = false;
-                break;
-              }
+            // (which has read the K in tile B's place, if one was there), and behind
+            // the PV that reads the V there
+            if (quant(kFmt) && pairs &&
+                !mbar_wait(&ct.vc_free[1], ((v_ring.parities >> 1) & 1) ^ 1, p.flags)) {
+              ok = false;
+              break;
             }
             if (lane == 0) {
               mbar_arrive_expect_tx(&ct.q_full, (uint32_t)(pairs ? 2 : 1) * Sm::kQB);
@@ -803,6 +803,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           __syncwarp();
           used |= 1u << st;
           ring.advance(depth);
+          v_ring.advance(v_buffers(pairs));
         }
       }
       // No copy may be on its way to this CTA's shared memory when it ends.  (One
@@ -817,7 +818,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       const uint32_t id_s = idesc_f16kind(kRows, kKeys, 0, !quant(kFmt));
       const uint32_t id_o = idesc_f16kind(kRows, D, 1, !quant(kFmt));
       const uint32_t q_addr = smem_u32(sq);
-      Ring kring, vring;        // bf16: slots of the next K and V tile
+      Ring kring, vring;        // slots of the next K and V tile (quantised: V's buffers)
       uint32_t jk = 0, jv = 0;  // key tiles so far, as S and as PV sees them
       uint32_t steps0 = 0, steps1 = 0;  // of each slot, before this segment
       uint32_t k_addr = 0, v_addr = 0;
@@ -829,7 +830,8 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         const bool pairs = sg.rows > kRows;
         const int depth = ring_depth(pairs);
         kring.enter(depth);
-        vring.enter(depth);
+        const int v_depth = quant(kFmt) ? v_buffers(pairs) : depth;
+        vring.enter(v_depth);
         const int nsteps = pairs ? 2 * sg.n : sg.n;
         // whether a step is its tile's first / last
         auto first_of = [&](int s) { return !pairs || !(s & 1); };
@@ -872,8 +874,8 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         auto issue_pv = [&](int s) -> bool {
           if (first_of(s)) {
             if constexpr (quant(kFmt)) {
-              v_addr = smem_u32(sconv) + 2 * Sm::kTileB;
-              if (!mbar_wait(&ct.vc_full[0], jv & 1, p.flags)) return false;
+              v_addr = smem_u32(v_made(vring.slot));
+              if (!mbar_wait(&ct.vc_full[vring.slot], vring.parity(), p.flags)) return false;
             } else {
               if (!mbar_wait(&ct.v_full[vring.slot], vring.parity(), p.flags)) return false;
               const int32_t key0 = (sg.tile0 + (pairs ? s >> 1 : s)) * kKeys;
@@ -904,12 +906,12 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
             for (int kk = 0; kk < kKeys / 16; ++kk)
               mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, bd + (kk * 2048 >> 4), id_o,
                      (s >= 2 || kk > 0) ? 1u : 0u);
-            if (last_of(s)) tc_commit(quant(kFmt) ? &ct.vc_free[0] : &ct.v_empty[vring.slot]);
+            if (last_of(s)) tc_commit(quant(kFmt) ? &ct.vc_free[vring.slot] : &ct.v_empty[vring.slot]);
             if (s + 2 >= nsteps) tc_commit(&ct.o_full[x]);  // the slot's last step
           }
           __syncwarp();
           if (last_of(s)) {
-            vring.advance(depth);
+            vring.advance(v_depth);
             ++jv;
           }
           return true;
@@ -937,18 +939,17 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
     // One warpgroup converts K, the other V and, at a segment's start, Q.
     const bool v = warp >= kConvWarp0 + kConvWarps;
     const int t = threadIdx.x & (kConvThreads - 1);
-    const uint32_t to = smem_u32(sconv) + (v ? 2 * Sm::kTileB : 0);
     uint64_t* const full = v ? ct.v_full : ct.k_full;
     uint64_t* const empty = v ? ct.v_empty : ct.k_empty;
     uint64_t* const made = v ? ct.vc_full : ct.kc_full;
     uint64_t* const free = v ? ct.vc_free : ct.kc_free;
-    const uint32_t buffers = v ? 1 : 2;
-    Ring ring;
-    uint32_t j = 0, buf = 0, use = 0;  // key tiles so far; buffer and its use's parity
+    Ring ring, out;  // slots of the codes, buffers of what they become
+    uint32_t j = 0;  // key tiles so far
     bool ok = true;
     Segment sg{};
-    sg.n = 1;
-    bool dry = true;  // as in the softmax: the first pass only fetches instructions
+    bool dry = take_segment(0, &sg);  // as in the softmax: the first pass only fetches
+    ok = dry;
+    sg.rows = kRows, sg.n = 1;
     for (uint32_t k = 0; ok; k += dry ? 0 : 1, dry = false) {
       if (!dry) {
         if (!take_segment(k, &sg)) break;
@@ -957,16 +958,14 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       }
       const int tiles_q = sg.rows > kRows ? 2 : 1;
       const int depth = ring_depth(tiles_q == 2);
+      const int buffers = v ? v_buffers(tiles_q == 2) : 2;
       ring.enter(depth);
+      out.enter(buffers);
       if (v) {
-        // Q to f16 in place, a row a thread, times the power of two that puts the
-        // row's largest value in [2^14, 2^15): bf16's 8 bits fit f16's 11, and what
-        // is small enough to lose bits is 2^-28 of the largest.
         if (!dry && !mbar_wait(&ct.q_full, k & 1, p.flags)) break;
-        for (int x = 0; x < tiles_q; ++x) {
-          const int e = q_row_to_f16<D>(smem_u32(sq) + x * Sm::kQB, t, !dry);
-          if (!dry) ct.q_exp[k & 1][x][t] = (int8_t)e;
-        }
+        for (int x = 0; x < tiles_q; ++x)
+          q_rows_to_f16<D>(smem_u32(sq) + x * Sm::kQB, t, min(kRows, sg.rows - x * kRows),
+                           ct.q_exp[k & 1][x], !dry);
         fence_async_smem();
         __syncwarp();
         if (lane == 0 && !dry) mbar_arrive(&ct.qc_full);
@@ -977,7 +976,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         int live = 3;
         if (!dry) {
           if (!mbar_wait(&full[st], ring.parity(), p.flags) ||
-              !mbar_wait(&free[buf], use ^ 1, p.flags)) {
+              !mbar_wait(&free[out.slot], out.parity() ^ 1, p.flags)) {
             ok = false;
             break;
           }
@@ -985,18 +984,18 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           live = ~ct.facts[j % kFactsRing].bad &
                  ((sg.tile0 + i) * kKeys + 64 < sg.prefix ? 3 : 1);
         }
-        convert_codes<D, kFmt>(smem_u32(v ? v_slot(st) : k_slot(st)), to + buf * Sm::kTileB, t,
-                               live);
+        const uint8_t* to = v ? v_made(out.slot) : sconv + out.slot * Sm::kTileB;
+        convert_codes<D, kFmt>(smem_u32(v ? v_slot(st) : k_slot(st)), smem_u32(to), t, live);
         fence_async_smem();
         __syncwarp();
         if (dry) break;
         if (lane == 0) {
-          mbar_arrive(&made[buf]);
+          mbar_arrive(&made[out.slot]);
           mbar_arrive(&empty[st]);
         }
         ring.advance(depth);
         ++j;
-        if (++buf == buffers) buf = 0, use ^= 1;
+        out.advance(buffers);
       }
     }
   }
