@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     Ce = C < T ? C : T;
     // With shared prefixes, as many as fit the SMs that the prefix kernel leaves.
     if (p.cu_groups && T > 0) {
-      const int sms = p.num_sms - divide_sms<D, kFmt>(p, lane).prefix_sms;
+      const int sms = p.num_sms - divide_sms<kFmt>(p, lane).prefix_sms;
       Ce = min(Ce, (int64_t)max(1, sms * p.ctas_per_sm));
     }
     if (c < Ce) {

@@ -54,67 +54,85 @@ __device__ __forceinline__ GroupWork group_work(const DecodeParams& p, int g) {
   return w;
 }
 
-// The two kernels run side by side: the prefix kernel's CTAs (one per SM) that
-// find no work leave at once, and decode CTAs take their SMs.  Both work out
-// the same division, in time of one SM; results do not depend on it.
+// The two kernels run side by side: prefix CTAs (one per SM) that find no work
+// leave at once, and decode CTAs take their SMs.  Both kernels work out the same
+// division, in SM-microseconds as measured on B200 at D = 128; results do not
+// depend on it.
 struct Division {
   int64_t steps;   // of the prefix kernel
   bool pairs;      // some group has two Q tiles
   int prefix_sms;  // SMs for the prefix kernel
 };
 
-// Measured SM-microseconds (B200, D = 128): a 128-key tile costs the prefix
-// kernel its bytes at the SM's share of HBM (44 GB/s a thousandth: 1.48 for bf16,
-// 0.74 for one-byte codes), 0.95 for a quantised tile's conversion, and 0.57 a Q
-// tile for the products and the softmax, whichever is most; it costs the decode
-// kernel its bytes, or about 1.5 for quantised codes, and each unit's end 0.5.
+// A 128-key tile against one or two Q tiles in the prefix kernel.  One: bf16 its
+// bytes at the SM's share of HBM (1.48), quantised 1.45 (one-byte codes) and 1.75
+// (FP4), the converters.  Two: 2.3 and 3.1, the hand-offs between products and
+// softmax.
 template <int kFmt>
-__device__ __forceinline__ float prefix_tile_cost(const DecodeParams& p, int q_tiles, int d) {
-  const float bytes = 2.f * 128.f * (row_code_bytes(kFmt, d) + row_scale_bytes(kFmt, d));
-  const float once = fmaxf(bytes * (1.f / 44300.f), quant(kFmt) ? 0.95f * d / 128.f : 0.f);
-  return fmaxf(once, 0.57f * q_tiles);
+__host__ __device__ constexpr float prefix_tile_cost(bool two) {
+  return two ? (quant(kFmt) ? 3.1f : 2.3f) : fp4(kFmt) ? 1.75f : 1.48f;
 }
-
+// The same tile in the decode kernel: bf16 its bytes, quantised its arithmetic;
+// and the end of a sequence's tiles.
 template <int kFmt>
-__device__ __forceinline__ float own_tile_cost(int d) {
-  const float bytes = 2.f * 128.f * (row_code_bytes(kFmt, d) + row_scale_bytes(kFmt, d));
-  return fmaxf(bytes * (1.f / 44300.f), quant(kFmt) ? 1.5f * d / 128.f : 0.f);
-}
-constexpr float kOwnUnitCost = 0.5f;
+__host__ __device__ constexpr float own_tile_cost() { return quant(kFmt) ? 1.1f : 1.48f; }
+template <int kFmt>
+__host__ __device__ constexpr float own_unit_cost() { return quant(kFmt) ? 0.9f : 0.4f; }
+// The prefix kernel's way to its first product and from its last is longer.
+template <int kFmt>
+__host__ __device__ constexpr float prefix_lead() { return quant(kFmt) ? 2.5f : 0.5f; }
 
 // Warp-wide.
-template <int D, int kFmt>
+template <int kFmt>
 __device__ Division divide_sms(const DecodeParams& p, int lane) {
   float own = 0.f, pre = 0.f;
-  int64_t steps = 0;
+  int64_t steps = 0, tiles = 0;
   bool two = false;
   const int32_t cap = p.max_pages * p.page_size;
   for (int b = lane; b < p.batch; b += 32) {
     const int32_t len = max(0, min(__ldg(p.seq_lens + b), cap));
-    if (len > 0) own += (float)((len + 127) / 128) * own_tile_cost<kFmt>(D) + kOwnUnitCost;
+    if (len > 0) own += (float)((len + 127) / 128) * own_tile_cost<kFmt>() + own_unit_cost<kFmt>();
   }
   for (int g = lane; g < p.num_groups; g += 32) {
     const GroupWork w = group_work(p, g);
     if (w.steps == 0) continue;
     steps += w.steps;
+    tiles += (int64_t)w.tiles * ((w.q_tiles + 1) >> 1);
     two |= w.q_tiles > 1;
-    own -= (float)(w.b1 - w.b0) * w.tiles * own_tile_cost<kFmt>(D);
-    for (int q = 0; q < w.q_tiles; q += 2)
-      pre += w.tiles * prefix_tile_cost<kFmt>(p, min(2, w.q_tiles - q), D);
+    own -= (float)(w.b1 - w.b0) * w.tiles * own_tile_cost<kFmt>();
+    pre += w.tiles * ((w.q_tiles >> 1) * prefix_tile_cost<kFmt>(true) +
+                      (w.q_tiles & 1) * prefix_tile_cost<kFmt>(false));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     own += __shfl_xor_sync(0xffffffffu, own, o);
     pre += __shfl_xor_sync(0xffffffffu, pre, o);
     steps += __shfl_xor_sync(0xffffffffu, steps, o);
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
   }
   Division d;
   d.steps = steps * p.num_kv_heads;
   d.pairs = __any_sync(0xffffffffu, two);
-  own = fmaxf(own, 0.f);
-  const int sms = p.num_sms;
-  d.prefix_sms = (int)rintf(sms * pre / fmaxf(pre + own, 1e-6f));
-  d.prefix_sms = max(d.steps > 0 ? 1 : 0, min(d.prefix_sms, own > 0.f ? sms - 1 : sms));
+  own = fmaxf(own, 0.f) * p.num_kv_heads;
+  const float n_tiles = (float)tiles * p.num_kv_heads;
+  const float tile = tiles > 0 ? __fdividef(pre, (float)tiles) : 0.f;
+  // The count whose later end comes first; a lane tries every 32nd.
+  const int most = (int)fminf((float)(own > 0.f ? p.num_sms - 1 : p.num_sms), n_tiles);
+  float best = 3.4e38f;
+  int at = most;
+  for (int n = 1 + lane; n <= most; n += 32) {
+    const float a = ceilf(__fdividef(n_tiles, (float)n)) * tile + prefix_lead<kFmt>();
+    const float c = own > 0.f ? __fdividef(own, (float)(p.num_sms - n)) : 0.f;
+    const float t = fmaxf(a, c);
+    if (t < best) best = t, at = n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float t = __shfl_xor_sync(0xffffffffu, best, o);
+    const int n = __shfl_xor_sync(0xffffffffu, at, o);
+    if (t < best || (t == best && n < at)) best = t, at = n;
+  }
+  d.prefix_sms = d.steps > 0 ? max(1, at) : 0;
   return d;
 }
 

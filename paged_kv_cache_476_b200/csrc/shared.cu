@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
   Cursor cur{};
   int b_table = -1;
   if (warp == kSchedWarp) {
-    const Division dv = divide_sms<D, kFmt>(p, lane);
+    const Division dv = divide_sms<kFmt>(p, lane);
     const int64_t T = dv.steps;
     // Every range holds a whole tile (two steps of an item with two Q tiles).
     const int64_t most = min((int)gridDim.x, dv.prefix_sms);
