@@ -191,6 +191,21 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 
 
+def _load_binding():
+    """The CPython module of the rotation and shared-prefix calls, on this library."""
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise ImportError(f"{_PKG}/_binding.so is missing or stale: build it with `python "
+                          "paged_kv_cache_476_b200/build.py`") from e
+    _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        _lib.pkv_qk_norm_rope, _lib.paged_kv_append_rope, _lib.paged_decode_attention_shared)))
+    return _binding
+
+
+_binding = _load_binding()
+
+
 def lib() -> ctypes.CDLL:
     return _lib
 
@@ -341,6 +356,7 @@ class PagedKVCache:
                            _KV_CODES[kv_dtype],
                            None if error_flags is None else error_flags.data_ptr())
         self._ref = ctypes.byref(self._c)
+        self._args = (ctypes.addressof(self._c), k_pool.device.index)
 
     @property
     def c_struct(self) -> PkvCache:
@@ -407,6 +423,11 @@ class Rope:
                           None if k_norm_weight is None else k_norm_weight.data_ptr(),
                           self.norm_eps)
         self._ref = ctypes.byref(self._c)
+        dims = {w.shape[0] for w in (q_norm_weight, k_norm_weight) if w is not None}
+        if len(dims) > 1:
+            raise ValueError("q_norm_weight and k_norm_weight must have the same length")
+        self._args = (ctypes.addressof(self._c), -1 if self.device is None else self.device.index,
+                      dims.pop() if dims else 0, int(cos_sin is not None))
 
     @property
     def c_struct(self) -> PkvRope:
@@ -431,6 +452,10 @@ def pkv_qk_norm_rope(rope: Rope, q, k, positions=None, q_out=None, k_out=None, e
     Returns ``(q_out, k_out)``; rows of tokens with a position outside the
     table keep what they held and raise ``PKV_FLAG_BAD_LENGTH``.
     """
+    if stream is None and q_out is None and k_out is None:
+        r = _binding.norm_rope(rope._args, q, k, positions, error_flags)
+        if r is not NotImplemented:
+            return r
     x = k if q is None else q
     if x is None:
         raise ValueError("q or k must be given")
@@ -480,6 +505,11 @@ def paged_kv_append_rope(cache: PagedKVCache, rope: Rope, page_table, seq_lens_b
     contiguous), None without ``q``.  Tokens behind ``cu_new_tokens[-1]`` (a
     padded batch) change nothing.
     """
+    if stream is None and q_out is None:
+        r = _binding.append_rope(cache._args, rope._args, page_table, seq_lens_before,
+                                 cu_new_tokens, k_new, v_new, q, positions, total_new_tokens)
+        if r is not NotImplemented:
+            return r
     _dev("page_table", page_table, torch.int32, 2)
     _dev("seq_lens_before", seq_lens_before, torch.int32, 1)
     _dev("cu_new_tokens", cu_new_tokens, torch.int32, 1)
@@ -635,6 +665,11 @@ def paged_decode_attention_shared(cache: PagedKVCache, q, page_table, seq_lens, 
     (``decode_shared_workspace``) serves one call at a time.  Returns
     ``(out bf16 [B, Hq, D], lse fp32 [B, Hq] or None)``.
     """
+    if stream is None and out is None and lse is None and workspace is not None:
+        r = _binding.decode_shared(cache._args, q, page_table, seq_lens, max_seq_len, cu_groups,
+                                   prefix_lens, softmax_scale, workspace, want_lse)
+        if r is not NotImplemented:
+            return r
     _dev("q", q, torch.bfloat16, 3)
     _dev("page_table", page_table, torch.int32, 2)
     for name, t in (("seq_lens", seq_lens), ("cu_groups", cu_groups),

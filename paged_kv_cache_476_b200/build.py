@@ -6,20 +6,26 @@ under ``csrc/`` compiles with nvcc and each host-only ``.cpp`` with g++ to an
 object in ``_build/`` (in parallel), then the
 objects link into ``paged_kv_cache_476_b200/libpagedkv.so`` with the CUDA
 runtime linked statically.  nvcc cross-compiles, so no GPU is needed.
+``csrc/python/binding.cpp`` becomes the CPython module ``_binding`` next to it
+(g++ against torch's headers; the library itself knows nothing of torch).
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
+BINDING_SRC = os.path.join(CSRC, "python", "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -61,13 +67,34 @@ def _compile(src, extra):
     return obj, ""
 
 
+def _build_binding(force):
+    """The CPython module; torch is located without importing it."""
+    if not (force or _stale(BINDING, [BINDING_SRC, *_headers()])):
+        return
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    dirs = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
+            os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+            os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+            sysconfig.get_paths()["include"]]
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared", *(f"-I{d}" for d in dirs),
+           BINDING_SRC, "-o", tmp, "-L" + os.path.join(torch, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, flags=()) -> str:
     """Compile every CUDA source and link ``libpagedkv.so``; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     extra = {"force": force, "flags": list(flags)}
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        binding = ex.submit(_build_binding, force)
         results = list(ex.map(lambda s: _compile(s, extra), srcs))
+        binding.result()
     objs = [o for o, _ in results]
     if verbose:
         for _, log in results:

@@ -323,3 +323,52 @@ def test_step_driver_rotates(pkv):
     assert torch.equal(pools[0].k, pools[1].k) and torch.equal(pools[0].v, pools[1].v)
     with pytest.raises(ValueError):
         drv.step([0], [], [], k, v, q=q)
+
+
+@pytest.mark.parametrize("T", [1, 37])
+def test_calls_on_a_given_stream_give_the_same(pkv, T):
+    """The binding's short way (this stream, its own results) and its long way."""
+    q, k, v = _fused(T, 8, 2, 128, 3)
+    rope = _rope(pkv, 128, 64, False, True)
+    pos = torch.arange(T, dtype=torch.int32).cuda()
+    here = torch.cuda.current_stream()
+    for a in ((q, k), (q, None), (None, k)):
+        for x, y in zip(pkv.pkv_qk_norm_rope(rope, *a, pos),
+                        pkv.pkv_qk_norm_rope(rope, *a, pos, stream=here)):
+            assert (x is None and y is None) or torch.equal(x, y)
+    pools = [_Pool(pkv, "bf16", 2, 2, 64, 128) for _ in range(2)]
+    table = torch.tensor([[1, 0]], dtype=torch.int32).cuda()
+    before = torch.tensor([5], dtype=torch.int32).cuda()
+    cu = torch.tensor([0, T], dtype=torch.int32).cuda()
+    x = pkv.paged_kv_append_rope(pools[0].cache, rope, table, before, cu, k, v, q=q)
+    y = pkv.paged_kv_append_rope(pools[1].cache, rope, table, before, cu, k, v, q=q, stream=here)
+    assert torch.equal(x, y) and torch.equal(pools[0].k, pools[1].k)
+    assert torch.equal(pools[0].v, pools[1].v)
+    assert pkv.paged_kv_append_rope(pools[0].cache, rope, table, before, cu, k, v) is None
+
+
+def test_refusals_from_python(pkv):
+    q, k, v = _fused(4, 8, 2, 128, 3)
+    rope = _rope(pkv, 128, 64, False, True)
+    pos = torch.arange(4, dtype=torch.int32).cuda()
+    for a in ((None, None, pos), (q, k, None), (q, k, pos[:3]), (q, k, pos.long()),
+              (q.float(), k, pos), (q, k[:3], pos), (q.cpu(), k, pos), (q[..., ::2], k, pos),
+              (q[..., :64].contiguous(), k[..., :64].contiguous(), pos)):
+        with pytest.raises(ValueError):
+            pkv.pkv_qk_norm_rope(rope, *a)
+    with pytest.raises(ValueError):
+        pkv.Rope(q_norm_weight=torch.ones(128).cuda(), k_norm_weight=torch.ones(64).cuda())
+    pool = _Pool(pkv, "bf16", 2, 2, 64, 128)
+    table = torch.tensor([[1, 0]], dtype=torch.int32).cuda()
+    before, cu = torch.zeros(1, dtype=torch.int32).cuda(), torch.tensor([0, 4]).int().cuda()
+    good = [table, before, cu, k, v]
+    for at, bad in ((0, table.long()), (0, table.repeat(2, 1)), (1, before.cpu()), (2, cu[:1]),
+                    (3, k[:, :1]), (4, v[:3]), (4, v.half())):
+        a = list(good)
+        a[at] = bad
+        with pytest.raises(ValueError):
+            pkv.paged_kv_append_rope(pool.cache, rope, *a)
+    for kw in ({"total_new_tokens": 5}, {"q": q[:3]}, {"q": q.float()}, {"positions": pos[:2]}):
+        with pytest.raises(ValueError):
+            pkv.paged_kv_append_rope(pool.cache, rope, *good, **kw)
+    assert int(pool.flags) == 0

@@ -306,3 +306,42 @@ def test_rotating_append_then_shared_decode(pkv, fmt):
         assert bool((err <= tol).all())
         assert bool(((lse[b].double().cpu().view(Hkv, G) - torch.logsumexp(s, -1)).abs()
                      <= ds[..., 0] + 2.0 ** -15).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_calls_on_a_given_stream_give_the_same(pkv, fmt):
+    """The binding's short way (this stream, its own results) and its long way."""
+    b = Batch([200, 210, 150], [0, 3], [128], 2, 4, 128, 64, fmt, seed=3)
+    cache = b.cache(pkv)
+    work = pkv.decode_shared_workspace(cache, 3, 8, 210, 1)
+    here = torch.cuda.current_stream()
+    short = pkv.paged_decode_attention_shared(cache, *b.args(), b.scale, workspace=work)
+    long = pkv.paged_decode_attention_shared(cache, *b.args(), b.scale, workspace=work, stream=here)
+    assert torch.equal(short[0], long[0]) and torch.equal(short[1], long[1])
+    none = pkv.paged_decode_attention_shared(cache, *b.args(), workspace=work, want_lse=False)
+    assert torch.equal(none[0], short[0]) and none[1] is None
+
+
+def test_refusals_from_python(pkv):
+    b = Batch([200, 210], [0, 2], [128], 2, 4, 128, 64, seed=3)
+    cache = b.cache(pkv)
+    work = pkv.decode_shared_workspace(cache, 2, 8, 210, 1)
+    q, table, lens, n, cu, prefix = b.args()
+    call = pkv.paged_decode_attention_shared
+    assert call(cache, q, table, lens, n, cu, prefix, workspace=work)[0].shape == q.shape
+    for args in ((q.float(), table, lens, n, cu, prefix), (q[:1], table, lens, n, cu, prefix),
+                 (q.cpu(), table, lens, n, cu, prefix), (q[..., :64], table, lens, n, cu, prefix),
+                 (q, table[:, ::2], lens, n, cu, prefix), (q, table.long(), lens, n, cu, prefix),
+                 (q, table, lens[:1], n, cu, prefix), (q, table, lens, n, cu[:2], prefix[:0]),
+                 (q, table, lens, n, cu, prefix.cpu())):
+        with pytest.raises(ValueError):
+            call(cache, *args, workspace=work)
+    with pytest.raises(ValueError):
+        call(cache, q, table, lens, n, cu, prefix, out=torch.empty_like(q)[:1])
+    with pytest.raises(ValueError):
+        call(cache, q, table, lens, n, cu, prefix, workspace=work.cpu())
+    for kw in ({"workspace": work[:64]}, {"softmax_scale": float("nan"), "workspace": work}):
+        with pytest.raises(pkv.PagedKVError):
+            call(cache, q, table, lens, n, cu, prefix, **kw)
+    with pytest.raises(pkv.PagedKVError):
+        call(cache, q, table, lens, table.shape[1] * 64 + 1, cu, prefix)
