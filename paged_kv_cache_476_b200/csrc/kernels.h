@@ -125,6 +125,7 @@ struct RopeParams {
   int32_t max_positions;
   int32_t rot;  // rotary_dim
   int32_t interleaved;
+  int32_t rows_per_item;  // set by the launch
   float eps;
   // The error word, and for the append the page geometry and pools, as there
   // (k_new, v_new and total_new are not used).

@@ -19,38 +19,40 @@
 // a lane, chosen so that both members of every pair sit in one lane: vectors
 // u and u + rot/16 of the rotated part (and likewise two of the rest).  The
 // rotation then needs no exchange, the norm log2(D/16) shuffles.  A lane
-// takes kRows rows of one token, so the table values (64 bytes a lane) and
-// the page lookup are fetched once for them and all their loads are in
-// flight together.
+// takes several rows of one token, so the table values (64 bytes a lane) and
+// the page lookup are fetched once for them.
 #include "common.cuh"
 #include "kernels.h"
+#include "tensor.cuh"
 
 namespace pkv {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+using pf::fma2;
+using pf::mul2;
 
-__device__ __forceinline__ void unpack8(const uint4& r, float* x) {
-  const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&r);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 f = __bfloat1622float2(p[k]);
-    x[2 * k] = f.x;
-    x[2 * k + 1] = f.y;
-  }
+constexpr int kRopeThreads = 256;
+// Blocks of an SM (80 or 128 registers a thread), rows a lane works on together,
+// and whether it loads the next ones meanwhile.  Measured (4,400 GB/s and up):
+// 16,384 tokens of 32 / 8 heads 65 us at (3, 2, no), 65 at (2, 2, yes), 79 at (2,
+// 1, yes); appends in bf16 of 8,900 tokens 46, 52, 61; in E4M3, where the codes'
+// arithmetic spills at 80 registers, of 740 tokens of 64 / 8 heads 22, 17, 18.
+template <int kFmt>
+struct Shape {
+  static constexpr bool kSpare = kFmt > 0;  // quantised pool
+  static constexpr int kBlocks = kSpare ? 2 : 3;
+  static constexpr int kRows = 2;
+  static constexpr bool kAhead = kSpare;
+};
+
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
 }
 
 __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                     pack_bf16(x[6], x[7]));
-}
-
-__device__ __forceinline__ void load8(const float* src, float* x) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(src));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(src) + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
 // Which 8-value vectors of a row of 2L vectors lane u holds: the first 2h
@@ -120,42 +122,45 @@ __device__ __forceinline__ float amax8(const float* x) {
 }
 
 // kFmt < 0: no cache, rotated k to k_out.
-template <int D, int kFmt, int kRows>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+template <int D, int kFmt, int kRows, bool kAhead, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads, Shape<kFmt>::kBlocks) rope_kernel(const RopeParams p) {
   constexpr bool kAppend = kFmt >= 0;
   constexpr int L = D / 16;
   const int lane = threadIdx.x & 31;
   const int u = lane & (L - 1);
-  // items: kRows rows of q, of k or (append) of v, of one token
-  const int nq = (p.num_q_heads + kRows - 1) / kRows;
-  const int nk = (p.num_kv_heads + kRows - 1) / kRows;
-  const int per_token = nq + (kAppend ? 2 : 1) * nk;
-  const int64_t item = (blockIdx.x * (int64_t)kRopeThreads + threadIdx.x) / L;
-  bool live = item < (int64_t)p.tokens * per_token;
+  // items: `per` rows of q, of k or (append) of v, of one token
+  const int per = p.rows_per_item;
+  const int nq = (p.num_q_heads + per - 1) / per;
+  const int nk = (p.num_kv_heads + per - 1) / per;
+  const uint32_t per_token = nq + (kAppend ? 2 : 1) * nk;
+  const uint32_t item = (blockIdx.x * (uint32_t)kRopeThreads + threadIdx.x) / L;
+  bool live = item < (uint32_t)p.tokens * per_token;
   const int tok = live ? (int)(item / per_token) : 0;
-  const int part = live ? (int)(item - (int64_t)tok * per_token) : 0;
+  const int part = live ? (int)(item - tok * per_token) : 0;
   const int kind = part < nq ? 0 : part < nq + nk ? 1 : 2;  // q, k, v
-  const int row0 = (part - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * kRows;
+  const int row0 = (part - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * per;
   const int heads = kind == 0 ? p.num_q_heads : p.num_kv_heads;
+  const int rows = live ? min(per, heads - row0) : 0;
 
-  // All of the item's loads, before anything waits on them.
+  // The first rows' loads go out before anything waits.
   const Halves<L> hv{kind == 2 ? L : p.rot / 16};
   const int va = hv.first(u), vb = hv.second(u);
+  const uint4* const src = reinterpret_cast<const uint4*>(
+      (kind == 0   ? p.q + tok * p.q_stride
+       : kind == 1 ? p.k + tok * p.k_stride
+                   : p.v + tok * p.v_stride) + (int64_t)row0 * D);
   uint4 ra[kRows], rb[kRows];
-  {
-    const __nv_bfloat16* src = kind == 0   ? p.q + tok * p.q_stride
-                               : kind == 1 ? p.k + tok * p.k_stride
-                                           : p.v + tok * p.v_stride;
+  auto load = [&](int r0, uint4* a, uint4* b) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      ra[r] = rb[r] = make_uint4(0, 0, 0, 0);
-      if (live && row0 + r < heads) {
-        const uint4* x = reinterpret_cast<const uint4*>(src + (int64_t)(row0 + r) * D);
-        ra[r] = x[va];  // plain loads: the output may be the input's buffer
-        rb[r] = x[vb];
+      a[r] = b[r] = make_uint4(0, 0, 0, 0);
+      if (r0 + r < rows) {
+        a[r] = src[(r0 + r) * (D / 8) + va];  // plain loads: the output may be the input's buffer
+        b[r] = src[(r0 + r) * (D / 8) + vb];
       }
     }
-  }
+  };
+  load(0, ra, rb);
 
   // Position of the token, and (append) its place in the cache.
   int64_t pos = 0;
@@ -168,12 +173,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       const int64_t at = (int64_t)__ldg(p.a.seq_lens_before + b) + (tok - __ldg(p.a.cu_new + b));
       pos = p.positions ? __ldg(p.positions + tok) : at;
       if (kind != 0) {
-        const int64_t j = at / p.a.page_size;
         const bool report = kind == 1 && row0 == 0 && u == 0;
-        if (at < 0 || j >= p.a.max_pages) {
+        if (at < 0 || at >= (int64_t)p.a.max_pages * p.a.page_size) {
           if (report) flag_error(p.a.flags, PKV_FLAG_BAD_LENGTH);
         } else {
-          slot = (int)(at - j * p.a.page_size);
+          const int shift = p.a.page_size == 128 ? 7 : 6;  // (64 otherwise)
+          const int j = (int)at >> shift;
+          slot = (int)at - (j << shift);
           page = __ldg(p.a.page_table + (int64_t)b * p.a.max_pages + j);
           if (page < 0 || page >= p.a.num_pages) {
             if (report) flag_error(p.a.flags, PKV_FLAG_BAD_PAGE);
@@ -192,154 +198,201 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     live = false;
   }
 
-  // cos and sin of this lane's eight pairs
+  // What a lane's 16 values are multiplied with: z_a = x_a P + y_a Q and z_b =
+  // x_b R + y_b S, where y is the pair's other value.  P, Q, R and S hold cosine
+  // and sine times the weight of the value they meet, so that with the row's
+  // 1 / rms a value costs three operations; two values go in one instruction.
   const bool turns = kind != 2 && u < p.rot / 16;
-  float cs[8], sn[8];
+  const float* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
+  float2 P[4], Q[4], R[4], S[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    P[i] = R[i] = make_float2(1.f, 1.f);
+    Q[i] = S[i] = make_float2(0.f, 0.f);
+  }
+  if (weight) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(weight + 8 * va) + h);
+      const float4 y = __ldg(reinterpret_cast<const float4*>(weight + 8 * vb) + h);
+      P[2 * h] = make_float2(x.x, x.y), P[2 * h + 1] = make_float2(x.z, x.w);
+      R[2 * h] = make_float2(y.x, y.y), R[2 * h + 1] = make_float2(y.z, y.w);
+    }
+  }
   if (turns && live) {
     const float* row = p.cos_sin + pos * p.rot;
-    if (p.interleaved) {
-      const float4 c0 = __ldg(reinterpret_cast<const float4*>(row + 4 * va));
-      const float4 c1 = __ldg(reinterpret_cast<const float4*>(row + 4 * vb));
-      const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + p.rot / 2 + 4 * va));
-      const float4 s1 = __ldg(reinterpret_cast<const float4*>(row + p.rot / 2 + 4 * vb));
-      cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w;
-      cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
-      sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w;
-      sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
+    if constexpr (kInterleaved) {
+      // pairs (2i, 2i + 1) of one vector: z = x (c, c) + swapped x (-s, s)
+      auto turn = [&](int v, float2* x, float2* y) {
+        const float4 c = __ldg(reinterpret_cast<const float4*>(row + 4 * v));
+        const float4 n = __ldg(reinterpret_cast<const float4*>(row + p.rot / 2 + 4 * v));
+        const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {n.x, n.y, n.z, n.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[i] = make_float2(-x[i].y * sn[i], x[i].x * sn[i]);
+          x[i] = make_float2(x[i].x * cs[i], x[i].y * cs[i]);
+        }
+      };
+      turn(va, P, Q);
+      turn(vb, R, S);
     } else {
-      load8(row + 8 * u, cs);
-      load8(row + p.rot / 2 + 8 * u, sn);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 c = __ldg(reinterpret_cast<const float4*>(row + 8 * u) + h);
+        const float4 n = __ldg(reinterpret_cast<const float4*>(row + p.rot / 2 + 8 * u) + h);
+        const float2 cs[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
+        const float2 sn[2] = {make_float2(n.x, n.y), make_float2(n.z, n.w)};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 x = P[2 * h + i], y = R[2 * h + i];
+          P[2 * h + i] = make_float2(x.x * cs[i].x, x.y * cs[i].y);
+          Q[2 * h + i] = make_float2(-y.x * sn[i].x, -y.y * sn[i].y);
+          R[2 * h + i] = make_float2(y.x * cs[i].x, y.y * cs[i].y);
+          S[2 * h + i] = make_float2(x.x * sn[i].x, x.y * sn[i].y);
+        }
+      }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = sn[i] = 0.f;
-  }
-  const float* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
-  float wa[8], wb[8];
-  if (weight) {
-    load8(weight + 8 * va, wa);
-    load8(weight + 8 * vb, wb);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.f;
   }
 
+  // (every lane of a warp takes as many turns: the shuffles are its groups' own,
+  // but rows of a warp may differ in kind)
+  const int turns_all = __reduce_max_sync(0xffffffffu, rows);
+  for (int r0 = 0; r0 < turns_all; r0 += kRows) {
+    uint4 na[kRows], nb[kRows];
+    if (kAhead) load(r0 + kRows, na, nb);  // the next rows, while these are worked on
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const bool row_live = live && row0 + r < heads;
-    float xa[8], xb[8];
-    unpack8(ra[r], xa);
-    unpack8(rb[r], xb);
-    if (kind != 2) {
+    for (int r = 0; r < kRows; ++r) {
+      const bool row_live = live && r0 + r < rows;
+      const uint32_t* wa = reinterpret_cast<const uint32_t*>(&ra[r]);
+      const uint32_t* wb = reinterpret_cast<const uint32_t*>(&rb[r]);
       // every lane takes the shuffles: rows of a warp may differ in kind
-      if (weight) {
-        float ss = 0.f;
+      float inv = 1.f;
+      if (kind != 2 && weight) {
+        float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
+        for (int i = 0; i < 4; ++i) {
+          const float2 xa = bf16_pair(wa[i]), xb = bf16_pair(wb[i]);
+          ss = fma2(xa, xa, ss);
+          ss = fma2(xb, xb, ss);
+        }
+        float sum = ss.x + ss.y;
         const uint32_t mask = (L == 32 ? 0xffffffffu : ((1u << L) - 1)) << (lane & ~(L - 1));
 #pragma unroll
-        for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(mask, ss, o);
-        const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          xa[i] *= inv * wa[i];
-          xb[i] *= inv * wb[i];
-        }
+        for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(mask, sum, o);
+        inv = rsqrtf(sum * (1.f / D) + p.eps);
       }
-      if (turns) {
-        if (p.interleaved) {
+      float xa[8], xb[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a0 = xa[2 * i], a1 = xa[2 * i + 1], b0 = xb[2 * i], b1 = xb[2 * i + 1];
-            xa[2 * i] = a0 * cs[i] - a1 * sn[i];
-            xa[2 * i + 1] = a1 * cs[i] + a0 * sn[i];
-            xb[2 * i] = b0 * cs[4 + i] - b1 * sn[4 + i];
-            xb[2 * i + 1] = b1 * cs[4 + i] + b0 * sn[4 + i];
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = bf16_pair(wa[i]), b = bf16_pair(wb[i]);
+        float2 za = a, zb = b;
+        if (kind != 2) {
+          const float2 inv2 = make_float2(inv, inv);
+          za = mul2(a, P[i]);
+          zb = mul2(b, R[i]);
+          if (turns) {  // (a branch, not zeros: 0 times an infinity is NaN)
+            const float2 ya = kInterleaved ? make_float2(a.y, a.x) : b;
+            const float2 yb = kInterleaved ? make_float2(b.y, b.x) : a;
+            za = fma2(ya, Q[i], za);
+            zb = fma2(yb, S[i], zb);
+          }
+          za = mul2(za, inv2);
+          zb = mul2(zb, inv2);
+        }
+        xa[2 * i] = za.x, xa[2 * i + 1] = za.y;
+        xb[2 * i] = zb.x, xb[2 * i + 1] = zb.y;
+      }
+      if (kind == 0 || !kAppend) {
+        if (row_live) {
+          __nv_bfloat16* out = kind == 0 ? p.q_out + (int64_t)tok * p.num_q_heads * D
+                                         : p.k_out + (int64_t)tok * p.num_kv_heads * D;
+          uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)(row0 + r0 + r) * D);
+          dst[va] = pack8(xa);
+          dst[vb] = pack8(xb);
+        }
+      } else if constexpr (kAppend) {
+        const int g = row0 + r0 + r;
+        uint8_t* pool = kind == 1 ? p.a.k_pool : p.a.v_pool;
+        const int64_t prow = ((int64_t)page * p.num_kv_heads + g) * p.a.page_size + slot;
+        if constexpr (kFmt == PKV_KV_BF16) {
+          if (row_live) {
+            uint4* dst = reinterpret_cast<uint4*>(pool + prow * D * 2);
+            dst[va] = kind == 1 ? pack8(xa) : ra[r];  // V: the input bits
+            dst[vb] = kind == 1 ? pack8(xb) : rb[r];
           }
         } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float a = xa[i], b = xb[i];
-            xa[i] = a * cs[i] - b * sn[i];
-            xb[i] = b * cs[i] + a * sn[i];
+          float s = 1.f;
+          if (row_live) {
+            s = __ldg((kind == 1 ? p.a.k_scale : p.a.v_scale) +
+                      (int64_t)page * p.num_kv_heads + g);
+            if (!(s > 0.f && s <= 32768.f) && u == 0) flag_error(p.a.flags, PKV_FLAG_BAD_SCALE);
+          }
+          float da = 0.f, db = 0.f;
+          if constexpr (fp4(kFmt)) {
+            // a block is vectors 2m and 2m + 1; the other one's largest value
+            // comes from the lane (of this row) that holds it
+            const uint32_t mask = ((1u << L) - 1) << (lane & ~(L - 1));
+            const float ma = amax8(xa), mb = amax8(xb);
+            const int ja = hv.lane(va ^ 1), jb = hv.lane(vb ^ 1);
+            const float fa0 = __shfl_sync(mask, ma, ja, L), fa1 = __shfl_sync(mask, mb, ja, L);
+            const float fb0 = __shfl_sync(mask, ma, jb, L), fb1 = __shfl_sync(mask, mb, jb, L);
+            uint32_t sba, sbb;
+            da = nvfp4_block_unit(fmaxf(ma, hv.slot(va ^ 1) ? fa1 : fa0), s, &sba);
+            db = nvfp4_block_unit(fmaxf(mb, hv.slot(vb ^ 1) ? fb1 : fb0), s, &sbb);
+            if (row_live) {
+              uint8_t* blocks = (kind == 1 ? p.a.k_blocks : p.a.v_blocks) + prow * (D / 16);
+              if (!(va & 1)) blocks[va >> 1] = (uint8_t)sba;
+              if (!(vb & 1)) blocks[vb >> 1] = (uint8_t)sbb;
+            }
+          }
+          if (row_live) {
+            store_codes<kFmt>(pool, prow, D, va, xa, s, da);
+            store_codes<kFmt>(pool, prow, D, vb, xb, s, db);
           }
         }
       }
     }
-    if (kind == 0 || !kAppend) {
-      if (row_live) {
-        __nv_bfloat16* out = kind == 0 ? p.q_out + (int64_t)tok * p.num_q_heads * D
-                                       : p.k_out + (int64_t)tok * p.num_kv_heads * D;
-        uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)(row0 + r) * D);
-        dst[va] = pack8(xa);
-        dst[vb] = pack8(xb);
-      }
-    } else if constexpr (kAppend) {
-      const int g = row0 + r;
-      uint8_t* pool = kind == 1 ? p.a.k_pool : p.a.v_pool;
-      const int64_t prow = ((int64_t)page * p.num_kv_heads + g) * p.a.page_size + slot;
-      if constexpr (kFmt == PKV_KV_BF16) {
-        if (row_live) {
-          uint4* dst = reinterpret_cast<uint4*>(pool + prow * D * 2);
-          dst[va] = kind == 1 ? pack8(xa) : ra[r];  // V: the input bits
-          dst[vb] = kind == 1 ? pack8(xb) : rb[r];
-        }
-      } else {
-        float s = 1.f;
-        if (row_live) {
-          s = __ldg((kind == 1 ? p.a.k_scale : p.a.v_scale) +
-                    (int64_t)page * p.num_kv_heads + g);
-          if (!(s > 0.f && s <= 32768.f) && u == 0) flag_error(p.a.flags, PKV_FLAG_BAD_SCALE);
-        }
-        float da = 0.f, db = 0.f;
-        if constexpr (fp4(kFmt)) {
-          // a block is vectors 2m and 2m + 1; the other one's largest value
-          // comes from the lane (of this row) that holds it
-          const uint32_t mask = ((1u << L) - 1) << (lane & ~(L - 1));
-          const float ma = amax8(xa), mb = amax8(xb);
-          const int ja = hv.lane(va ^ 1), jb = hv.lane(vb ^ 1);
-          const float fa0 = __shfl_sync(mask, ma, ja, L), fa1 = __shfl_sync(mask, mb, ja, L);
-          const float fb0 = __shfl_sync(mask, ma, jb, L), fb1 = __shfl_sync(mask, mb, jb, L);
-          uint32_t sba, sbb;
-          da = nvfp4_block_unit(fmaxf(ma, hv.slot(va ^ 1) ? fa1 : fa0), s, &sba);
-          db = nvfp4_block_unit(fmaxf(mb, hv.slot(vb ^ 1) ? fb1 : fb0), s, &sbb);
-          if (row_live) {
-            uint8_t* blocks = (kind == 1 ? p.a.k_blocks : p.a.v_blocks) + prow * (D / 16);
-            if (!(va & 1)) blocks[va >> 1] = (uint8_t)sba;
-            if (!(vb & 1)) blocks[vb >> 1] = (uint8_t)sbb;
-          }
-        }
-        if (row_live) {
-          store_codes<kFmt>(pool, prow, D, va, xa, s, da);
-          store_codes<kFmt>(pool, prow, D, vb, xb, s, db);
-        }
-      }
+    if (kAhead) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) ra[r] = na[r], rb[r] = nb[r];
     }
   }
 }
 
-template <int D, int kFmt, int kRows>
-cudaError_t rope_launch(const RopeParams& p, cudaStream_t stream) {
-  const int nq = (p.num_q_heads + kRows - 1) / kRows;
-  const int nk = (p.num_kv_heads + kRows - 1) / kRows;
-  const int64_t items = (int64_t)p.tokens * (nq + (kFmt >= 0 ? 2 : 1) * nk);
+template <int D, int kFmt, int kRows, bool kAhead>
+cudaError_t rope_launch(const RopeParams& p, int64_t items, cudaStream_t stream) {
   const int64_t blocks = (items * (D / 16) + kRopeThreads - 1) / kRopeThreads;
   if (blocks == 0) return cudaSuccess;
-  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  rope_kernel<D, kFmt, kRows><<<(unsigned)blocks, kRopeThreads, 0, stream>>>(p);
+  if (blocks * kRopeThreads > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (p.interleaved)
+    rope_kernel<D, kFmt, kRows, kAhead, true>
+        <<<(unsigned)blocks, kRopeThreads, 0, stream>>>(p);
+  else
+    rope_kernel<D, kFmt, kRows, kAhead, false>
+        <<<(unsigned)blocks, kRopeThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 // kFmt -1: no cache
 template <int kFmt>
-cudaError_t rope_run(const RopeParams& p, int head_dim, int num_sms, cudaStream_t stream) {
-  const int64_t rows =
-      (int64_t)p.tokens * (p.num_q_heads + (kFmt >= 0 ? 2 : 1) * p.num_kv_heads);
-  // One row a lane while that still leaves SMs idle; then four.
-  const bool few = rows * (head_dim / 16) <= (int64_t)num_sms * 1024;
+cudaError_t rope_run(RopeParams p, int head_dim, int num_sms, cudaStream_t stream) {
+  auto items = [&](int per) -> int64_t {
+    const int nq = (p.num_q_heads + per - 1) / per, nk = (p.num_kv_heads + per - 1) / per;
+    return (int64_t)p.tokens * (nq + (kFmt >= 0 ? 2 : 1) * nk);
+  };
+  // As many rows an item as leave every SM a block and a half: the way to the
+  // first product costs a lane as much as two rows.
+  const int64_t enough = (int64_t)num_sms * kRopeThreads * 3 / 2 / (head_dim / 16);
+  int per = 8;
+  while (per > 1 && items(per) < enough) per /= 2;
+  p.rows_per_item = per;
+  const int64_t n = items(per);
+  using Sh = Shape<kFmt>;
   if (head_dim == 128)
-    return few ? rope_launch<128, kFmt, 1>(p, stream) : rope_launch<128, kFmt, 4>(p, stream);
-  return few ? rope_launch<64, kFmt, 1>(p, stream) : rope_launch<64, kFmt, 4>(p, stream);
+    return per > 1 ? rope_launch<128, kFmt, Sh::kRows, Sh::kAhead>(p, n, stream)
+                   : rope_launch<128, kFmt, 1, false>(p, n, stream);
+  return per > 1 ? rope_launch<64, kFmt, Sh::kRows, Sh::kAhead>(p, n, stream)
+                 : rope_launch<64, kFmt, 1, false>(p, n, stream);
 }
 
 }  // namespace
