@@ -82,6 +82,15 @@ __host__ __device__ constexpr float own_unit_cost() { return quant(kFmt) ? 0.9f 
 template <int kFmt>
 __host__ __device__ constexpr float prefix_lead() { return quant(kFmt) ? 2.5f : 0.5f; }
 
+// Sum over the warp of counts (exact): one instruction where they are small.
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+  if (__all_sync(0xffffffffu, x < (1 << 26)))
+    return __reduce_add_sync(0xffffffffu, (uint32_t)x);
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
 // Warp-wide.
 template <int kFmt>
 __device__ Division divide_sms(const DecodeParams& p, int lane) {
@@ -89,17 +98,18 @@ __device__ Division divide_sms(const DecodeParams& p, int lane) {
   int64_t steps = 0, tiles = 0;
   bool two = false;
   const int32_t cap = p.max_pages * p.page_size;
+#pragma unroll 1
   for (int b = lane; b < p.batch; b += 32) {
     const int32_t len = max(0, min(__ldg(p.seq_lens + b), cap));
     if (len > 0) own += (float)((len + 127) / 128) * own_tile_cost<kFmt>() + own_unit_cost<kFmt>();
   }
+#pragma unroll 1
   for (int g = lane; g < p.num_groups; g += 32) {
     const GroupWork w = group_work(p, g);
-    if (w.steps == 0) continue;
     steps += w.steps;
     tiles += (int64_t)w.tiles * ((w.q_tiles + 1) >> 1);
     two |= w.q_tiles > 1;
-    own -= (float)(w.b1 - w.b0) * w.tiles * own_tile_cost<kFmt>();
+    own -= (float)(w.q_tiles > 0 ? w.b1 - w.b0 : 0) * w.tiles * own_tile_cost<kFmt>();
     pre += w.tiles * ((w.q_tiles >> 1) * prefix_tile_cost<kFmt>(true) +
                       (w.q_tiles & 1) * prefix_tile_cost<kFmt>(false));
   }
@@ -107,32 +117,21 @@ __device__ Division divide_sms(const DecodeParams& p, int lane) {
   for (int o = 16; o > 0; o >>= 1) {
     own += __shfl_xor_sync(0xffffffffu, own, o);
     pre += __shfl_xor_sync(0xffffffffu, pre, o);
-    steps += __shfl_xor_sync(0xffffffffu, steps, o);
-    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
   }
   Division d;
-  d.steps = steps * p.num_kv_heads;
+  d.steps = warp_sum(steps) * p.num_kv_heads;
   d.pairs = __any_sync(0xffffffffu, two);
+  const float n_tiles = (float)warp_sum(tiles) * p.num_kv_heads;
   own = fmaxf(own, 0.f) * p.num_kv_heads;
-  const float n_tiles = (float)tiles * p.num_kv_heads;
-  const float tile = tiles > 0 ? __fdividef(pre, (float)tiles) : 0.f;
-  // The count whose later end comes first; a lane tries every 32nd.
-  const int most = (int)fminf((float)(own > 0.f ? p.num_sms - 1 : p.num_sms), n_tiles);
-  float best = 3.4e38f;
-  int at = most;
-  for (int n = 1 + lane; n <= most; n += 32) {
-    const float a = ceilf(__fdividef(n_tiles, (float)n)) * tile + prefix_lead<kFmt>();
-    const float c = own > 0.f ? __fdividef(own, (float)(p.num_sms - n)) : 0.f;
-    const float t = fmaxf(a, c);
-    if (t < best) best = t, at = n;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float t = __shfl_xor_sync(0xffffffffu, best, o);
-    const int n = __shfl_xor_sync(0xffffffffu, at, o);
-    if (t < best || (t == best && n < at)) best = t, at = n;
-  }
-  d.prefix_sms = d.steps > 0 ? max(1, at) : 0;
+  pre *= p.num_kv_heads;
+  // n SMs for the prefix so that both end together: pre / n + lead = own / (sms - n),
+  // a quadratic in n; then no more of them than make the same number of tiles each.
+  const float sms = (float)p.num_sms, lead = prefix_lead<kFmt>();
+  const float h = lead * sms - pre - own;
+  float n = own > 0.f ? (h + sqrtf(h * h + 4.f * lead * pre * sms)) / (2.f * lead) : sms;
+  n = fmaxf(1.f, fminf(fminf(rintf(n), own > 0.f ? sms - 1.f : sms), n_tiles));
+  n = ceilf(__fdividef(n_tiles, ceilf(__fdividef(n_tiles, n))));
+  d.prefix_sms = d.steps > 0 ? max(1, min((int)n, p.num_sms)) : 0;
   return d;
 }
 

@@ -52,7 +52,7 @@ using namespace pf;
 // pools add a warpgroup of converters.
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
-constexpr int kSchedWarp = 10;  // warp 11 has no role
+constexpr int kSchedWarp = 10;  // warp 11 only checks the groups
 constexpr int kConvWarp0 = 12;
 constexpr int kConvWarps = 4;  // for K, and as many for V
 constexpr int kConvThreads = kConvWarps * 32;
@@ -103,6 +103,7 @@ struct Control {
   TileFacts facts[kFactsRing];
   Segment seg[kSegRing];
   uint32_t tmem;
+  int32_t idle;  // this CTA's range is empty
   // quantised pools: Q rows are 2^q_exp times f16, by segment parity and tile
   int8_t q_exp[2][2][kRows];
 };
@@ -223,6 +224,15 @@ __device__ Cursor locate(const DecodeParams& p, int64_t x, int lane) {
   c.head = c.pair = c.tile = 0;
   c.item_x = run;
   return c;
+}
+
+// Groups that run backwards or leave the batch, and negative prefixes.  Warp-wide.
+__device__ void check_groups(const DecodeParams& p, int lane) {
+  for (int g = lane; g < p.num_groups; g += 32) {
+    const int32_t b0 = __ldg(p.cu_groups + g), b1 = __ldg(p.cu_groups + g + 1);
+    if (b0 < 0 || b1 < b0 || b1 > p.batch || __ldg(p.prefix_lens + g) < 0)
+      flag_error(p.flags, PKV_FLAG_BAD_LENGTH);
+  }
 }
 
 // First sequence of a group that holds the whole prefix, whose table row names
@@ -419,6 +429,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
     fence_barrier_init();
   }
   if (warp == kMmaWarp) tmem_alloc(&ct.tmem, kTmemCols);
+  if (warp == kSchedWarp + 1 && blockIdx.x == 0) check_groups(p, lane);
   if (warp == kProducerWarp && lane == 0) {
     tma_prefetch_desc(&tmap_q);
     tma_prefetch_desc(&tmap_k);
@@ -444,12 +455,22 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
     if (x < x_end) {
       cur = locate(p, x, lane);
       b_table = first_holder(p, cur.w, lane);
+      // the producer's first page ids
+      const int64_t key0 = (int64_t)cur.tile * kKeys + lane * 64;
+      if (b_table >= 0 && key0 < cur.w.prefix)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(
+            p.page_table + (int64_t)b_table * p.max_pages + key0 / p.page_size));
     }
+    if (lane == 0) ct.idle = x < x_end ? 0 : 1;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ct.tmem;
+  if (ct.idle) {  // its SM goes to the decode kernel
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
   // Segment number `k` (each warp that works on segments takes every one).
   auto take_segment = [&](uint32_t k, Segment* sg) -> bool {
     if (!mbar_wait(&ct.seg_full[k % kSegRing], (k / kSegRing) & 1, p.flags)) return false;
@@ -678,12 +699,6 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         ++k;
         if (s.n == 0) break;
       }
-      if (c == 0)
-        for (int g = lane; g < p.num_groups; g += 32) {
-          const int32_t b0 = __ldg(p.cu_groups + g), b1 = __ldg(p.cu_groups + g + 1);
-          if (b0 < 0 || b1 < b0 || b1 > p.batch || __ldg(p.prefix_lens + g) < 0)
-            flag_error(p.flags, PKV_FLAG_BAD_LENGTH);
-        }
     } else if (warp == kProducerWarp) {
       // ------------------------------------------------------------- producer
       // The whole warp walks the tiles, lane 0 issues.  A lane looks up one of 32
