@@ -380,8 +380,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     // real tile); a unit's segment count is the number of ranges that hold
     // its real tiles, and every range between its first and last holds some.
     Ce = C < T ? C : T;
-    // With shared prefixes, as many as fit the SMs that the prefix kernel leaves.
-    if (p.cu_groups && T > 0) {
+    // With shared prefixes, as many as fit the SMs that the prefix kernel leaves
+    // (a few tiles are one each wherever they run).
+    if (p.cu_groups && T > p.num_sms) {
       const int sms = p.num_sms - divide_sms<kFmt>(p, lane).prefix_sms;
       Ce = min(Ce, (int64_t)max(1, sms * p.ctas_per_sm));
     }

@@ -64,23 +64,24 @@ struct Division {
   int prefix_sms;  // SMs for the prefix kernel
 };
 
-// A 128-key tile against one or two Q tiles in the prefix kernel.  One: bf16 its
-// bytes at the SM's share of HBM (1.48), quantised 1.45 (one-byte codes) and 1.75
-// (FP4), the converters.  Two: 2.3 and 3.1, the hand-offs between products and
-// softmax.
+// A 128-key tile against one or two Q tiles in the prefix kernel: bf16 its bytes
+// at the SM's share of HBM (1.48) and the hand-offs between products and softmax
+// (2.35); quantised the converters.
 template <int kFmt>
 __host__ __device__ constexpr float prefix_tile_cost(bool two) {
-  return two ? (quant(kFmt) ? 3.1f : 2.3f) : fp4(kFmt) ? 1.75f : 1.48f;
+  return !quant(kFmt) ? (two ? 2.35f : 1.48f) : two ? 3.1f : fp4(kFmt) ? 1.75f : 1.45f;
 }
 // The same tile in the decode kernel: bf16 its bytes, quantised its arithmetic;
 // and the end of a sequence's tiles.
 template <int kFmt>
-__host__ __device__ constexpr float own_tile_cost() { return quant(kFmt) ? 1.1f : 1.48f; }
+__host__ __device__ constexpr float own_tile_cost() {
+  return quant(kFmt) ? 1.05f : 1.25f;
+}
 template <int kFmt>
-__host__ __device__ constexpr float own_unit_cost() { return quant(kFmt) ? 0.9f : 0.4f; }
-// The prefix kernel's way to its first product and from its last is longer.
+__host__ __device__ constexpr float own_unit_cost() { return quant(kFmt) ? 0.85f : 0.35f; }
+// How much longer the prefix kernel's way to its first product and from its last is.
 template <int kFmt>
-__host__ __device__ constexpr float prefix_lead() { return quant(kFmt) ? 2.5f : 0.5f; }
+__host__ __device__ constexpr float prefix_lead() { return quant(kFmt) ? 2.5f : 1.5f; }
 
 // Sum over the warp of counts (exact): one instruction where they are small.
 __device__ __forceinline__ int64_t warp_sum(int64_t x) {

@@ -962,8 +962,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
     uint32_t j = 0;  // key tiles so far
     bool ok = true;
     Segment sg{};
-    bool dry = take_segment(0, &sg);  // as in the softmax: the first pass only fetches
-    ok = dry;
+    bool dry = true;  // as in the softmax: the first pass only fetches, here at once
     sg.rows = kRows, sg.n = 1;
     for (uint32_t k = 0; ok; k += dry ? 0 : 1, dry = false) {
       if (!dry) {
@@ -1059,8 +1058,9 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   // Where the parts lie (a CTA that gave up may have left its word unwritten).
   int n_pre = 0, n_own = 0, per = 1, rows = 0;  // parts; parts and rows of a segment
   int64_t pre_row = 0, own_row = 0;
+  const int4 info = __ldcg(sp.pre_info + u);  // first row, segments, first sequence, rows
+  const int2 own = __ldcg(p.unit_info + u);   // (both read whether of use or not: one trip)
   if (shared > 0) {
-    const int4 info = __ldcg(sp.pre_info + u);  // first row, segments, first sequence, rows
     rows = info.w;
     per = rows > kRows ? 1 : 2;
     if (info.x >= 0 && info.y > 0 && info.y <= kMaxSegments && b >= info.z &&
@@ -1071,12 +1071,9 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
       rows |= (b - info.z) * G << 16;  // low half: rows, high half: this unit's first row
     }
   }
-  if (len > shared) {
-    const int2 info = __ldcg(p.unit_info + u);
-    if (info.x >= 0 && info.y > 0 && (int64_t)info.x + info.y <= sp.own_slots) {
-      n_own = info.y;
-      own_row = (int64_t)info.x * G;
-    }
+  if (len > shared && own.x >= 0 && own.y > 0 && (int64_t)own.x + own.y <= sp.own_slots) {
+    n_own = own.y;
+    own_row = (int64_t)own.x * G;
   }
   const int r0 = rows >> 16;
   rows &= 0xffff;
@@ -1106,8 +1103,10 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   const int my_row = threadIdx.x % G, my_part = threadIdx.x / G;
   constexpr int kStep = kMergeThreads / G;
   float M = -INFINITY;
+  // (the first of them stays here: few units have more)
+  const float2 my_ml = my_part < n ? ml_of(my_part, my_row) : make_float2(0.f, 0.f);
   for (int i = my_part; i < n; i += kStep) {
-    const float2 ml = ml_of(i, my_row);
+    const float2 ml = i == my_part ? my_ml : ml_of(i, my_row);
     if (ml.y != 0.f) M = fmaxf(M, ml.x);  // l = 0: a part without keys, its o is not written
   }
 #pragma unroll
@@ -1125,7 +1124,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
     const int cn = min(n - c0, kChunk);
     if (c0 > 0) __syncthreads();  // the last chunk's weights have been used
     for (int i = my_part; i < cn; i += kStep) {
-      const float2 ml = ml_of(c0 + i, my_row);
+      const float2 ml = c0 + i == my_part ? my_ml : ml_of(c0 + i, my_row);
       const float w = ml.y != 0.f ? fast_exp2(ml.x - M) : 0.f;
       s_w[i * G + my_row] = w;
       L += w * ml.y;
