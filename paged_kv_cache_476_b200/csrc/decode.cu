@@ -182,18 +182,16 @@ __device__ __forceinline__ int32_t clamp_len(const DecodeParams& p, int32_t len,
 }
 
 // Tokens this call attends to for sequence b: all of them, or, in a batch with
-// shared prefixes, those behind the prefix (the first page_offset(p, b) pages
-// of its table row), which another kernel reads once for its group.
+// shared prefixes, those behind the prefix, which another kernel reads once for
+// its group.
 __device__ __forceinline__ int32_t own_len(const DecodeParams& p, int b, bool report) {
   const int32_t len = clamp_len(p, __ldg(p.seq_lens + b), report);
   if (!p.cu_groups) return len;
   return len - shared_tokens(p, b, len);
 }
 
-__device__ __forceinline__ int32_t page_offset(const DecodeParams& p, int b) {
-  if (!p.cu_groups) return 0;
-  const int32_t len = clamp_len(p, __ldg(p.seq_lens + b), false);
-  return shared_tokens(p, b, len) / p.page_size;
+__device__ __forceinline__ int32_t planned_len(const DecodeParams& p, const int32_t* lens, int b) {
+  return lens ? lens[b] : own_len(p, b, false);
 }
 
 // The work list counts each unit as its tiles plus kCost virtual tiles after
@@ -215,12 +213,12 @@ struct TilePos {
 };
 
 template <int kTile, int kCost>
-__device__ TilePos locate_tile(const DecodeParams& p, int64_t v, int lane) {
+__device__ TilePos locate_tile(const DecodeParams& p, const int32_t* lens, int64_t v, int lane) {
   const int Hkv = p.num_kv_heads;
   int64_t run_v = 0, run_r = 0;
   for (int base = 0; base < p.batch; base += 32) {
     const int b = base + lane;
-    const int t = b < p.batch ? tiles_of<kTile>(own_len(p, b, false)) : 0;
+    const int t = b < p.batch ? tiles_of<kTile>(planned_len(p, lens, b)) : 0;
     const int vt = t > 0 ? t + kCost : 0;  // virtual tiles of one unit of b
     int incl_v = vt, incl_r = t;
 #pragma unroll
@@ -254,7 +252,7 @@ __device__ TilePos locate_tile(const DecodeParams& p, int64_t v, int lane) {
         r.g = 0;
         do {
           ++r.b;
-        } while (r.b < p.batch && tiles_of<kTile>(own_len(p, r.b, false)) == 0);
+        } while (r.b < p.batch && tiles_of<kTile>(planned_len(p, lens, r.b)) == 0);
       }
       return r;
     }
@@ -365,12 +363,23 @@ __global__ void __launch_bounds__(kThreads, 2)
   int64_t n_tiles = 0;
   int pb = 0, pg = 0, pt = 0;  // producer's position (b, g, tile) at the range start
   int64_t range_start = 0, T = 0, Ce = 1;
+  // With shared prefixes a length takes a search among the groups: every thread
+  // of the CTA makes some, once.
+  const int32_t* lens = nullptr;
+  constexpr int kPlanned = kStages * Ly::kStageB / 4;  // in place of the tiles
+  if (p.cu_groups && p.batch <= kPlanned) {
+    int32_t* made = reinterpret_cast<int32_t*>(tiles);
+    for (int b = threadIdx.x; b < p.batch; b += kThreads) made[b] = own_len(p, b, c == 0);
+    __syncthreads();
+    lens = made;
+  }
   if (warp == kProducerWarp) {
     // Total virtual tiles over all units (real tiles plus the end costs).
     int64_t tot = 0;
     for (int base = 0; base < p.batch; base += 32) {
       const int b = base + lane;
-      const int t = b < p.batch ? tiles_of<kTile>(own_len(p, b, c == 0)) : 0;
+      const int32_t len = b >= p.batch ? 0 : lens ? lens[b] : own_len(p, b, c == 0);
+      const int t = tiles_of<kTile>(len);
       tot += t > 0 ? t + unit_end_cost<kFmt>() : 0;
     }
 #pragma unroll
@@ -388,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (c < Ce) {
       constexpr int kCost = unit_end_cost<kFmt>();
-      const TilePos s0 = locate_tile<kTile, kCost>(p, (c * T) / Ce, lane);
-      const TilePos s1 = locate_tile<kTile, kCost>(p, ((c + 1) * T) / Ce, lane);
+      const TilePos s0 = locate_tile<kTile, kCost>(p, lens, (c * T) / Ce, lane);
+      const TilePos s1 = locate_tile<kTile, kCost>(p, lens, ((c + 1) * T) / Ce, lane);
       n_tiles = s1.real - s0.real;
       pb = s0.b;
       pg = s0.g;
@@ -410,6 +419,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     if (lane == 0) s_misc[0] = (int)n_tiles;
+    // (the lengths' place is the loads' from here on)
+    if (lens) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   __syncthreads();
   n_tiles = s_misc[0];
@@ -484,7 +495,26 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     const int P = p.page_size;
     int b = pb, g = pg, t = pt;
-    int len = own_len(p, b, false);
+    // With shared prefixes a lane holds the own length and the first own page of
+    // one of 32 consecutive sequences.
+    int span_b0 = 0, my_own = 0, my_page = 0;
+    auto look_up = [&](int at) {
+      span_b0 = at;
+      const int x = at + lane;
+      my_own = my_page = 0;
+      if (x < p.batch) {
+        my_own = own_len(p, x, false);
+        my_page = (clamp_len(p, __ldg(p.seq_lens + x), false) - my_own) / p.page_size;
+      }
+    };
+    auto len_of = [&](int x) -> int {  // (x does not decrease)
+      if (!p.cu_groups) return own_len(p, x, false);
+      if (x >= span_b0 + 32) look_up(x);
+      return __shfl_sync(0xffffffffu, my_own, x - span_b0);
+    };
+    if (p.cu_groups) look_up(b);
+    int len = len_of(b);
+    int first_page = p.cu_groups ? __shfl_sync(0xffffffffu, my_page, b - span_b0) : 0;
     int ntile = tiles_of<kTile>(len);
     int seg_first_t = t;
     // page ids (and scales) of 32 consecutive pages, one per lane
@@ -512,8 +542,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         cache_key = key;
         cache_j0 = j_first;
         const int jj = j_first + lane;
-        my_pid = jj < pages_b ? __ldg(p.page_table + (int64_t)b * p.max_pages +
-                                       page_offset(p, b) + jj) : 0;
+        my_pid =
+            jj < pages_b ? __ldg(p.page_table + (int64_t)b * p.max_pages + first_page + jj) : 0;
         if constexpr (quant(kFmt)) {
           if (jj < pages_b && my_pid >= 0 && my_pid < p.num_pages) {
             my_ks = __ldg(p.k_scale + (int64_t)my_pid * Hkv + g);
@@ -646,9 +676,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           g = 0;
           do {
             ++b;
-          } while (b < p.batch && tiles_of<kTile>(own_len(p, b, false)) == 0);
+            len = b < p.batch ? len_of(b) : 0;
+          } while (b < p.batch && tiles_of<kTile>(len) == 0);
           if (b < p.batch) {
-            len = own_len(p, b, false);
+            if (p.cu_groups) first_page = __shfl_sync(0xffffffffu, my_page, b - span_b0);
             ntile = tiles_of<kTile>(len);
           }
         }

@@ -1025,28 +1025,45 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
 }
 
 // ------------------------------------------------------------------- merge
-// One CTA per (sequence, kv head): adds up the prefix partials of its G rows
-// and the partials of the sequence's own tokens.  The (m, l) of all parts come
-// first, spread over the threads, and give every part its weight
-// 2^(m_i - M); the sum over the o_i then has no chain through it: the warps
-// take parts in turn, eight vectors in flight a lane, and add up in shared
-// memory.  Launched as a programmatic dependent of the decode kernel, whose
-// completion (and memory) it awaits.
+// One to four warps (kW, by the unit's G * D outputs) per (sequence, kv head)
+// add up the prefix partials of its G rows and the partials of the sequence's own
+// tokens.  The (m, l) of all parts come first, spread over the threads, and give
+// every part its weight 2^(m_i - M); the sum over the o_i then has no chain
+// through it: the warps take parts in turn, eight vectors in flight a lane, and
+// add up in shared memory.  Launched as a programmatic dependent of the decode
+// kernel, whose completion (and memory) it awaits.
 constexpr int kMergeThreads = 128;
-constexpr int kMergeWarps = kMergeThreads / 32;
+
+__host__ __device__ constexpr int merge_warps(int gd) { return gd >= 512 ? 4 : gd >= 256 ? 2 : 1; }
 
 template <int D, int G>
 __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const SharedParams sp) {
-  constexpr int kChunk = 2048 / G;         // parts whose weights fit the shared array
-  constexpr int kVecs = G * D / 4;         // float4 vectors of the unit's output
-  constexpr int kN = (kVecs + 31) / 32;    // of a lane
+  constexpr int kW = merge_warps(G * D);
+  constexpr int kThreads = 32 * kW;             // of a unit
+  constexpr int kUnits = kMergeThreads / kThreads;
+  constexpr int kChunk = 2048 / G / kUnits;     // parts whose weights fit the shared array
+  constexpr int kVecs = G * D / 4;              // float4 vectors of the unit's output
+  constexpr int kN = (kVecs + 31) / 32;         // of a lane
   constexpr int kInFlight = kN >= 8 ? 1 : 8 / kN;  // parts a lane loads together
-  __shared__ float s_w[kChunk * G];
-  __shared__ float s_red[2][kMergeWarps][G];
-  __shared__ float4 s_acc[kMergeWarps][kVecs];
+  __shared__ float s_w_all[kUnits][kChunk * G];
+  __shared__ float s_red_all[kUnits][2][kW][G];
+  __shared__ float4 s_acc_all[kUnits][kW][kVecs];
   const DecodeParams& p = sp.d;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int u = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % kW;
+  const int tid = threadIdx.x % kThreads, slot = threadIdx.x / kThreads;
+  auto& s_w = s_w_all[slot];
+  auto& s_red = s_red_all[slot];
+  auto& s_acc = s_acc_all[slot];
+  auto unit_sync = [&]() {
+    if constexpr (kW == 4)
+      __syncthreads();
+    else if constexpr (kW == 2)
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + slot) : "memory");
+    else
+      __syncwarp();
+  };
+  const int u = blockIdx.x * kUnits + slot;
+  if (u >= p.batch * p.num_kv_heads) return;  // (the whole unit's threads)
   const int b = u / p.num_kv_heads;
   const int g = u - b * p.num_kv_heads;
   // (the arguments do not change under the kernels: read before the wait)
@@ -1098,10 +1115,10 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
     return __ldcg(p.part_ml + own_row + (int64_t)(i - n_pre) * G + row);
   };
 
-  // The largest reference of each row: thread t looks at row t % G.
+  // The largest reference of each row: thread t of a unit looks at row t % G.
   const int n = n_pre + n_own;
-  const int my_row = threadIdx.x % G, my_part = threadIdx.x / G;
-  constexpr int kStep = kMergeThreads / G;
+  const int my_row = tid % G, my_part = tid / G;
+  constexpr int kStep = kThreads / G;
   float M = -INFINITY;
   // (the first of them stays here: few units have more)
   const float2 my_ml = my_part < n ? ml_of(my_part, my_row) : make_float2(0.f, 0.f);
@@ -1112,9 +1129,9 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
 #pragma unroll
   for (int o = G; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (lane < G) s_red[0][warp][lane] = M;
-  __syncthreads();
+  unit_sync();
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) M = fmaxf(M, s_red[0][w][my_row]);
+  for (int w = 0; w < kW; ++w) M = fmaxf(M, s_red[0][w][my_row]);
 
   float4 acc[kN];
 #pragma unroll
@@ -1122,15 +1139,15 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   float L = 0.f;
   for (int c0 = 0; c0 < n; c0 += kChunk) {
     const int cn = min(n - c0, kChunk);
-    if (c0 > 0) __syncthreads();  // the last chunk's weights have been used
+    if (c0 > 0) unit_sync();  // the last chunk's weights have been used
     for (int i = my_part; i < cn; i += kStep) {
       const float2 ml = c0 + i == my_part ? my_ml : ml_of(c0 + i, my_row);
       const float w = ml.y != 0.f ? fast_exp2(ml.x - M) : 0.f;
       s_w[i * G + my_row] = w;
       L += w * ml.y;
     }
-    __syncthreads();
-    for (int i0 = warp * kInFlight; i0 < cn; i0 += kMergeWarps * kInFlight) {
+    unit_sync();
+    for (int i0 = warp * kInFlight; i0 < cn; i0 += kW * kInFlight) {
       float4 o[kInFlight][kN];
       float w[kInFlight][kN];
 #pragma unroll
@@ -1167,13 +1184,13 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
 #pragma unroll
   for (int j = 0; j < kN; ++j)
     if (kVecs >= 32 || lane < kVecs) s_acc[warp][lane + 32 * j] = acc[j];
-  __syncthreads();
-  for (int v = threadIdx.x; v < kVecs; v += kMergeThreads) {
+  unit_sync();
+  for (int v = tid; v < kVecs; v += kThreads) {
     const int row = v % G;
     float4 a = s_acc[0][v];
     float l = s_red[1][0][row];
 #pragma unroll
-    for (int w = 1; w < kMergeWarps; ++w) {
+    for (int w = 1; w < kW; ++w) {
       const float4 x = s_acc[w][v];
       a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
       l += s_red[1][w][row];
@@ -1182,7 +1199,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
     const float inv = l == 0.f ? 0.f : 1.f / l;
     *reinterpret_cast<uint2*>(p.out + orow * D + 4 * (v / G)) =
         make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-    // (M belongs to row threadIdx.x % G, which is v % G)
+    // (M belongs to row tid % G, which is v % G)
     if (p.lse && v < G)
       p.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
   }
@@ -1192,7 +1209,6 @@ template <int D>
 cudaError_t merge_for(const SharedParams& sp, cudaStream_t stream) {
   const int64_t units = (int64_t)sp.d.batch * sp.d.num_kv_heads;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)units);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1200,6 +1216,8 @@ cudaError_t merge_for(const SharedParams& sp, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  const int a_block = 4 / merge_warps(sp.d.group * D);
+  cfg.gridDim = dim3((unsigned)((units + a_block - 1) / a_block));
   switch (sp.d.group) {
     case 1: return cudaLaunchKernelEx(&cfg, shared_merge_kernel<D, 1>, sp);
     case 2: return cudaLaunchKernelEx(&cfg, shared_merge_kernel<D, 2>, sp);
