@@ -71,6 +71,9 @@ template <int kFmt>
 __host__ __device__ constexpr float prefix_tile_cost(bool two) {
   return !quant(kFmt) ? (two ? 2.35f : 1.48f) : two ? 3.1f : fp4(kFmt) ? 1.75f : 1.45f;
 }
+// A group's heads beyond the first of a CTA: queries to fetch, partials to write.
+template <int kFmt>
+__host__ __device__ constexpr float prefix_unit_cost() { return quant(kFmt) ? 3.f : 2.f; }
 // The same tile in the decode kernel: bf16 its bytes, quantised its arithmetic;
 // and the end of a sequence's tiles.
 template <int kFmt>
@@ -112,7 +115,8 @@ __device__ Division divide_sms(const DecodeParams& p, int lane) {
     two |= w.q_tiles > 1;
     own -= (float)(w.q_tiles > 0 ? w.b1 - w.b0 : 0) * w.tiles * own_tile_cost<kFmt>();
     pre += w.tiles * ((w.q_tiles >> 1) * prefix_tile_cost<kFmt>(true) +
-                      (w.q_tiles & 1) * prefix_tile_cost<kFmt>(false));
+                      (w.q_tiles & 1) * prefix_tile_cost<kFmt>(false)) +
+           ((w.q_tiles + 1) >> 1) * prefix_unit_cost<kFmt>();
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {

@@ -57,6 +57,13 @@ constexpr int kConvWarp0 = 12;
 constexpr int kConvWarps = 4;  // for K, and as many for V
 constexpr int kConvThreads = kConvWarps * 32;
 constexpr int kSegRing = 2;  // segment descriptors ahead
+// Barriers that say Q is converted.  A one-tile segment's queries give way to the
+// next one's once its S is issued, with no word from the softmax, and a slot
+// without steps holds nobody up: a softmax warp that is about to wait for segment
+// k's Q may find k + 1's and k + 2's converted (not k + 3's: its descriptor
+// waits for every warp to take k + 1's).  With fewer than four barriers the
+// parity it waits for could have gone by.
+constexpr int kQRing = 4;
 // A facts slot is refilled when the K ring has let go of a tile (at most
 // kMaxStages tiles back); the softmax may be three tiles behind that.
 constexpr int kMaxStages = 5;
@@ -93,7 +100,8 @@ struct Segment {
 // Barriers and small state in front of the tiles.
 struct Control {
   uint64_t seg_full[kSegRing], seg_empty[kSegRing];
-  uint64_t q_full, q_empty, qc_full;  // Q landed, free again, converted
+  uint64_t q_full, q_empty;       // Q landed, free again
+  uint64_t qc_full[kQRing];       // Q converted, by segment in turn
   uint64_t k_full[kMaxStages + 1], k_empty[kMaxStages + 1];
   uint64_t v_full[kMaxStages + 1], v_empty[kMaxStages + 1];
   uint64_t s_full[2], p_full[2], o_full[2];
@@ -405,7 +413,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
     }
     mbar_init(&ct.q_full, 1);
     mbar_init(&ct.q_empty, 1);
-    mbar_init(&ct.qc_full, kConvWarps);
+    for (int s = 0; s < kQRing; ++s) mbar_init(&ct.qc_full[s], kConvWarps);
     for (int s = 0; s < kMaxStages + 1; ++s) {
       mbar_init(&ct.k_full[s], 1);
       mbar_init(&ct.v_full[s], 1);
@@ -506,7 +514,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       float m_ref = -INFINITY, l = 0.f;
       float row_mul = p.scale_log2;
       if (quant(kFmt) && !dry) {  // (every segment: a phase left out would be mistaken later)
-        if (!mbar_wait(&ct.qc_full, k & 1, p.flags)) { ok = false; break; }
+        if (!mbar_wait(&ct.qc_full[k % kQRing], (k / kQRing) & 1, p.flags)) { ok = false; break; }
         row_mul = ldexpf(p.scale_log2, -ct.q_exp[k & 1][pairs ? x : 0][r]);
       }
       for (int q = 0; q < mine; ++q) {
@@ -932,7 +940,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           return true;
         };
         if (quant(kFmt))
-          ok = mbar_wait(&ct.qc_full, k & 1, p.flags);
+          ok = mbar_wait(&ct.qc_full[k % kQRing], (k / kQRing) & 1, p.flags);
         else
           ok = mbar_wait(&ct.q_full, k & 1, p.flags);
         if (ok) ok = issue_s(0);
@@ -982,7 +990,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
                            ct.q_exp[k & 1][x], !dry);
         fence_async_smem();
         __syncwarp();
-        if (lane == 0 && !dry) mbar_arrive(&ct.qc_full);
+        if (lane == 0 && !dry) mbar_arrive(&ct.qc_full[k % kQRing]);
       }
 #pragma unroll 1
       for (int i = 0; i < sg.n; ++i) {

@@ -345,3 +345,24 @@ def test_refusals_from_python(pkv):
             call(cache, q, table, lens, n, cu, prefix, **kw)
     with pytest.raises(pkv.PagedKVError):
         call(cache, q, table, lens, table.shape[1] * 64 + 1, cu, prefix)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("heads,G,D", [(8, 1, 64), (4, 4, 128)])
+def test_many_short_prefixes_again_and_again(pkv, fmt, heads, G, D):
+    """Many one- and two-tile prefixes for each CTA: its roles lead and lag across them."""
+    groups = 40
+    cu = [2 * i for i in range(groups + 1)]
+    prefix = [64 * (1 + i % 4) for i in range(groups)]
+    lens = [prefix[i // 2] + 1 + (37 * i) % 900 for i in range(2 * groups)]
+    b = Batch(lens, cu, prefix, heads, G, D, 64, fmt, seed=2)
+    cache = b.cache(pkv)
+    args = b.args()
+    work = pkv.decode_shared_workspace(cache, 2 * groups, heads * G, max(lens), groups)
+    first = pkv.paged_decode_attention_shared(cache, *args, b.scale, workspace=work)
+    assert_exact(first, b)
+    for _ in range(150):
+        again = pkv.paged_decode_attention_shared(cache, *args, b.scale, workspace=work)
+    torch.cuda.synchronize()
+    assert int(b.flags) == 0
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
