@@ -153,6 +153,11 @@ cudaError_t shared_merge_run(int head_dim, const SharedParams& p, cudaStream_t s
 cudaError_t launch_combine(const void* parts, const float* lse_parts, int num_parts, int rows,
                            int head_dim, void* out, float* lse, cudaStream_t stream);
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();  // null: not to be had
 int check_cache(const pkv_cache* c);
 int check_group(const pkv_cache* c, int32_t num_q_heads, int32_t gqa_group);
 int check_table_span(const pkv_cache* c, int32_t max_pages_per_seq);

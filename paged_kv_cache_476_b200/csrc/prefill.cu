@@ -849,19 +849,9 @@ int prefill_entry(const pkv_cache* cache, const void* q, int32_t num_q_heads, in
 }
 
 // 3-D view of the packed queries [total_q][Hq][D] with a [128/G][G][64] box.
-typedef CUresult (*EncodeTiledFnQ)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 int encode_q_map(CUtensorMap* map, const void* q, int total_q, int hq, int d, int group) {
-  void* fnp = nullptr;
-  cudaDriverEntryPointQueryResult qr;
-  if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fnp, cudaEnableDefault, &qr) !=
-          cudaSuccess ||
-      qr != cudaDriverEntryPointSuccess || !fnp)
-    return PKV_ERR_CUDA;
-  EncodeTiledFnQ fn = reinterpret_cast<EncodeTiledFnQ>(fnp);
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return PKV_ERR_CUDA;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)hq, (cuuint64_t)total_q};
   cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)hq * d * 2};
   cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(pf::kRows / group)};

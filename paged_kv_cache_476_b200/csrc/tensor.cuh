@@ -29,6 +29,7 @@ __device__ __forceinline__ bool elect_one() {
       : "+r"(one));
   return one != 0;
 }
+
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                    smem_u32(dst_smem)),
@@ -213,13 +214,13 @@ __device__ __forceinline__ uint32_t code_chunk(uint32_t base, int r, int c) {
 
 // E4M3 tile -> bf16 or f16 tile (both exact: every E4M3 value is an f16 and a
 // bf16), rows in `zero_mask` (bit per 64-row block) or at/after `zero_from`
-// written as zeros.  kThreads threads share the work.
-template <int D, int kFmt, bool kToF16, int kThreads = 64>
+// written as zeros.  64 threads share the work.
+template <int D, int kFmt, bool kToF16>
 __device__ __forceinline__ void convert_tile(uint32_t src, uint32_t dst, int t, int zero_from,
                                              int zero_mask) {
   constexpr int kChunks = kKeys * D / 16;  // 16-byte E4M3 chunks
 #pragma unroll 4
-  for (int ci = t; ci < kChunks; ci += kThreads) {
+  for (int ci = t; ci < kChunks; ci += 64) {
     const int r = ci / (D / 16);
     const int c = ci - r * (D / 16);
     uint32_t o[8];
@@ -259,15 +260,15 @@ __device__ __forceinline__ void convert_tile(uint32_t src, uint32_t dst, int t, 
 // FP4 tile (codes, then one E4M3 block scale per 16 values of a row) ->
 // bf16 or f16 tile, values e2m1(code) * decode(sb): exact in both, since the
 // product has at most 6 significant bits and lies in [2^-10, 2688].  Rows
-// in `zero_mask` or at/after `zero_from` are written as zeros.  kThreads threads.
-template <int D, bool kToF16, int kThreads = 64>
+// in `zero_mask` or at/after `zero_from` are written as zeros.  64 threads.
+template <int D, bool kToF16>
 __device__ __forceinline__ void convert_fp4_tile(uint32_t src, uint32_t dst, int t, int zero_from,
                                                  int zero_mask) {
   constexpr int kRowB = D / 2;            // code bytes of a row
   constexpr int kChunks = kKeys * D / 32;  // 16-byte chunks of codes (32 values, 2 blocks)
   const uint32_t scales = src + kKeys * kRowB;
 #pragma unroll 2
-  for (int ci = t; ci < kChunks; ci += kThreads) {
+  for (int ci = t; ci < kChunks; ci += 64) {
     const int r = ci / (D / 32);
     const int c = ci - r * (D / 32);
     uint32_t o[16];

@@ -348,20 +348,26 @@ def test_refusals_from_python(pkv):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("heads,G,D", [(8, 1, 64), (4, 4, 128)])
-def test_many_short_prefixes_again_and_again(pkv, fmt, heads, G, D):
-    """Many one- and two-tile prefixes for each CTA: its roles lead and lag across them."""
-    groups = 40
-    cu = [2 * i for i in range(groups + 1)]
-    prefix = [64 * (1 + i % 4) for i in range(groups)]
-    lens = [prefix[i // 2] + 1 + (37 * i) % 900 for i in range(2 * groups)]
+@pytest.mark.parametrize("heads,G,D,sizes", [(8, 1, 64, [2]), (4, 4, 128, [2]),
+                                             (2, 8, 128, [2, 20, 33, 3]), (2, 4, 64, [3, 70, 40]),
+                                             (3, 4, 128, [40, 2, 34, 2, 70])])
+def test_many_short_prefixes_again_and_again(pkv, fmt, heads, G, D, sizes):
+    """Many prefixes of one to five tiles for each CTA, against one and two Q tiles: its
+    roles lead and lag across them, and what lies where changes between them."""
+    groups = 40 if len(sizes) == 1 else 20
+    cu, lens, prefix = [0], [], []
+    for i in range(groups):
+        n = sizes[i % len(sizes)]
+        prefix.append(64 * (1 + (7 * i) % 10 // (2 if len(sizes) == 1 else 1)))
+        lens += [prefix[-1] + 1 + (37 * (cu[-1] + j)) % 900 for j in range(n)]
+        cu.append(cu[-1] + n)
     b = Batch(lens, cu, prefix, heads, G, D, 64, fmt, seed=2)
     cache = b.cache(pkv)
     args = b.args()
-    work = pkv.decode_shared_workspace(cache, 2 * groups, heads * G, max(lens), groups)
+    work = pkv.decode_shared_workspace(cache, cu[-1], heads * G, max(lens), groups)
     first = pkv.paged_decode_attention_shared(cache, *args, b.scale, workspace=work)
     assert_exact(first, b)
-    for _ in range(150):
+    for _ in range(100):
         again = pkv.paged_decode_attention_shared(cache, *args, b.scale, workspace=work)
     torch.cuda.synchronize()
     assert int(b.flags) == 0
