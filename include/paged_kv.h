@@ -317,8 +317,8 @@ int paged_decode_attention_append(const pkv_cache* cache, const void* q, int32_t
  *   prefix_lens  int32 [num_groups]; 0: nothing is shared
  *                (negative: 0, with PKV_FLAG_BAD_LENGTH)
  *   num_groups   0: paged_decode_attention
- *   workspace    paged_decode_shared_workspace_bytes(...) bytes, 16-byte
- *                aligned; one call at a time may use it
+ *   workspace    paged_decode_shared_workspace_bytes(...) bytes (0 on error, for
+ *                the current device), 16-byte aligned; one call at a time may use it
  * Results equal paged_decode_attention's up to the order of summation, and are
  * the same from run to run.  The other arguments, flags and errors are those of
  * paged_decode_attention.

@@ -197,7 +197,7 @@ PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!PyFloat_CheckExact(a[7])) return not_handled();
     scale = PyFloat_AS_DOUBLE(a[7]);
   }
-  const bool want_lse = a[9] == Py_True;
+  const bool want_lse = PyObject_IsTrue(a[9]) == 1;
   at::Tensor out = like(*q, q->sizes()), lse;
   if (want_lse) lse = at::empty({batch, heads}, q->options().dtype(at::kFloat));
   const int st = c_shared(

@@ -11,8 +11,12 @@
 // attends to each sequence's own tokens, and a merge adds the parts up.
 //
 // The prefix kernel.
-//  * Bound: HBM bytes of the prefix up to about 250 rows (n * G) of bf16, the
-//    tensor cores and the softmax above that.
+//  * Bound: HBM bytes of the prefix for one Q tile of bf16 (1.4 us a 128-key tile
+//    and SM at head_dim 128: the SM's share); the cycle of a slot, its softmax, the
+//    products and the hand-offs between them, for two (2.35 us a tile; 3.0 of
+//    quantised pools); the converters for one Q tile of quantised pools (1.45 us,
+//    FP4 1.75).  16 sequences behind 65,536 bf16 tokens of 8 kv heads: 54 us, 4.9
+//    TB/s, of which 6 us pass before the first tile has landed.
 //  * Items.  A group's rows of one kv head are cut into pairs of 128-row Q
 //    tiles, A and B.  An item is (group, kv head, pair) over the prefix's
 //    128-key tiles.  The items' steps (a tile times one Q tile) in order are
@@ -30,10 +34,12 @@
 //    to slot i & 1 whatever the mode: step i's PV, then step i + 2's S.
 //  * Each role walks the segments on its own; only barriers on the data tie
 //    them, so loads (and conversions) run ahead across segments.
-//  * Quantised K and V: four more warps convert codes exactly to f16, and Q's
-//    rows (times powers of two) with them; the K scales multiply the scores of
-//    their 64-key block, the V scales ride on P.  The softmax warps take the
-//    registers that the other warps give up.
+//  * Quantised K and V: four warps convert K's codes exactly to f16 and four V's
+//    and, at a segment's start, Q's rows (times powers of two); the K scales
+//    multiply the scores of their 64-key block, the V scales ride on P.  The
+//    softmax warps take the registers that the other warps give up.  (K and V
+//    apart: a conversion is 0.6 us and the hand-offs around it 0.4, and V's wait
+//    for the softmax must not hold K up.)
 //  * Every wait is bounded; a timeout ends the CTA with the error flag set.
 #include <mutex>
 
@@ -49,7 +55,7 @@ namespace sh {
 using namespace pf;
 
 // Warps: 0-3 and 4-7 softmax of slot 0 and 1, then the roles below; quantised
-// pools add a warpgroup of converters.
+// pools add two warpgroups of converters.
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kSchedWarp = 10;  // warp 11 only checks the groups
@@ -1038,8 +1044,10 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
 // tokens.  The (m, l) of all parts come first, spread over the threads, and give
 // every part its weight 2^(m_i - M); the sum over the o_i then has no chain
 // through it: the warps take parts in turn, eight vectors in flight a lane, and
-// add up in shared memory.  Launched as a programmatic dependent of the decode
-// kernel, whose completion (and memory) it awaits.
+// add up in shared memory.  Bound by its four trips to memory (7 us alone for 512
+// units of three parts; 62 us with a chain through the parts).  Launched as a
+// programmatic dependent of the decode kernel, whose completion (and memory) it
+// awaits.
 constexpr int kMergeThreads = 128;
 
 __host__ __device__ constexpr int merge_warps(int gd) { return gd >= 512 ? 4 : gd >= 256 ? 2 : 1; }

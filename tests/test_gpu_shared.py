@@ -372,3 +372,23 @@ def test_many_short_prefixes_again_and_again(pkv, fmt, heads, G, D, sizes):
     torch.cuda.synchronize()
     assert int(b.flags) == 0
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_nobody_holds_a_token(pkv):
+    """A padded batch: every length 0."""
+    for fmt in FORMATS:
+        b = Batch([0] * 5, [0, 3, 5], [64, 128], 2, 4, 128, 64, fmt, seed=1)
+        cache = b.cache(pkv)
+        out, lse = torch.full_like(b.q, 7), torch.zeros(5, 8, device="cuda")
+        pkv.paged_decode_attention_shared(cache, *b.args(), b.scale, out, lse)
+        assert int(b.flags) == 0
+        assert not bool(out.any()) and bool((lse == -torch.inf).all())
+
+
+@pytest.mark.parametrize("fmt,n", [("nvfp4", 4700), ("bf16", 700)])
+def test_many_sequences(pkv, fmt, n):
+    """More sequences than a CTA plans in shared memory (4,608 of FP4 at head_dim 64)."""
+    prefix, cu = [64, 0, 128], [5, n // 2, n // 2, n - 9]
+    lens = [(64 if i < n // 2 else 128) + i % 7 for i in range(n)]
+    lens[3], lens[n - 20] = 0, 100
+    _check(pkv, Batch(lens, cu, prefix, 1, 2, 64, 64, fmt, seed=4))
