@@ -184,14 +184,15 @@ __device__ __forceinline__ int32_t clamp_len(const DecodeParams& p, int32_t len,
 // Tokens this call attends to for sequence b: all of them, or, in a batch with
 // shared prefixes, those behind the prefix, which another kernel reads once for
 // its group.
+template <bool kGroups>
 __device__ __forceinline__ int32_t own_len(const DecodeParams& p, int b, bool report) {
   const int32_t len = clamp_len(p, __ldg(p.seq_lens + b), report);
-  if (!p.cu_groups) return len;
-  return len - shared_tokens(p, b, len);
+  return kGroups ? len - shared_tokens(p, b, len) : len;
 }
 
+template <bool kGroups>
 __device__ __forceinline__ int32_t planned_len(const DecodeParams& p, const int32_t* lens, int b) {
-  return lens ? lens[b] : own_len(p, b, false);
+  return kGroups && lens ? lens[b] : own_len<kGroups>(p, b, false);
 }
 
 // The work list counts each unit as its tiles plus kCost virtual tiles after
@@ -212,13 +213,13 @@ struct TilePos {
   int64_t xv, real;
 };
 
-template <int kTile, int kCost>
+template <int kTile, int kCost, bool kGroups>
 __device__ TilePos locate_tile(const DecodeParams& p, const int32_t* lens, int64_t v, int lane) {
   const int Hkv = p.num_kv_heads;
   int64_t run_v = 0, run_r = 0;
   for (int base = 0; base < p.batch; base += 32) {
     const int b = base + lane;
-    const int t = b < p.batch ? tiles_of<kTile>(planned_len(p, lens, b)) : 0;
+    const int t = b < p.batch ? tiles_of<kTile>(planned_len<kGroups>(p, lens, b)) : 0;
     const int vt = t > 0 ? t + kCost : 0;  // virtual tiles of one unit of b
     int incl_v = vt, incl_r = t;
 #pragma unroll
@@ -252,7 +253,7 @@ __device__ TilePos locate_tile(const DecodeParams& p, const int32_t* lens, int64
         r.g = 0;
         do {
           ++r.b;
-        } while (r.b < p.batch && tiles_of<kTile>(planned_len(p, lens, r.b)) == 0);
+        } while (r.b < p.batch && tiles_of<kTile>(planned_len<kGroups>(p, lens, r.b)) == 0);
       }
       return r;
     }
@@ -266,8 +267,8 @@ __device__ TilePos locate_tile(const DecodeParams& p, const int32_t* lens, int64
 // ends (a programmatic dependent of it that reads none of its results).  One
 // CTA stays until that kernel is complete, so that whoever waits for this
 // grid, the merge, has waited for both.
-__device__ __forceinline__ void await_prefix(const DecodeParams& p) {
-  if (p.cu_groups && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+__device__ __forceinline__ void await_prefix() {
+  if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Fused append: the producer warp writes sequence b's newest token (K and V
@@ -311,7 +312,9 @@ __device__ __forceinline__ void append_newest(const DecodeParams& p, int b, int 
   }
 }
 
-template <int D, int kFmt, int kStages, int kSnap>
+// kGroups: a call with shared prefixes (an instantiation of its own, so that the
+// plain call carries nothing for it).
+template <int D, int kFmt, int kStages, int kSnap, bool kGroups>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
                   const __grid_constant__ CUtensorMap tmap_v, const DecodeParams p) {
@@ -367,9 +370,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   // of the CTA makes some, once.
   const int32_t* lens = nullptr;
   constexpr int kPlanned = kStages * Ly::kStageB / 4;  // in place of the tiles
-  if (p.cu_groups && p.batch <= kPlanned) {
+  if (kGroups && p.batch <= kPlanned) {
     int32_t* made = reinterpret_cast<int32_t*>(tiles);
-    for (int b = threadIdx.x; b < p.batch; b += kThreads) made[b] = own_len(p, b, c == 0);
+    for (int b = threadIdx.x; b < p.batch; b += kThreads) made[b] = own_len<kGroups>(p, b, c == 0);
     __syncthreads();
     lens = made;
   }
@@ -378,7 +381,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     int64_t tot = 0;
     for (int base = 0; base < p.batch; base += 32) {
       const int b = base + lane;
-      const int32_t len = b >= p.batch ? 0 : lens ? lens[b] : own_len(p, b, c == 0);
+      const int32_t len = b >= p.batch       ? 0
+                          : kGroups && lens ? lens[b]
+                                            : own_len<kGroups>(p, b, c == 0);
       const int t = tiles_of<kTile>(len);
       tot += t > 0 ? t + unit_end_cost<kFmt>() : 0;
     }
@@ -391,14 +396,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     Ce = C < T ? C : T;
     // With shared prefixes, as many as fit the SMs that the prefix kernel leaves
     // (a few tiles are one each wherever they run).
-    if (p.cu_groups && T > p.num_sms) {
+    if (kGroups && T > p.num_sms) {
       const int sms = p.num_sms - divide_sms<kFmt>(p, lane).prefix_sms;
       Ce = min(Ce, (int64_t)max(1, sms * p.ctas_per_sm));
     }
     if (c < Ce) {
       constexpr int kCost = unit_end_cost<kFmt>();
-      const TilePos s0 = locate_tile<kTile, kCost>(p, lens, (c * T) / Ce, lane);
-      const TilePos s1 = locate_tile<kTile, kCost>(p, lens, ((c + 1) * T) / Ce, lane);
+      const TilePos s0 = locate_tile<kTile, kCost, kGroups>(p, lens, (c * T) / Ce, lane);
+      const TilePos s1 = locate_tile<kTile, kCost, kGroups>(p, lens, ((c + 1) * T) / Ce, lane);
       n_tiles = s1.real - s0.real;
       pb = s0.b;
       pg = s0.g;
@@ -407,9 +412,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     // Empty sequences (length 0): out = 0, lse = -inf, written by one CTA each
     // (with shared prefixes the merge writes every row).
-    if (!p.cu_groups) {
+    if (!kGroups) {
       for (int b = (int)((c * p.batch) / C); b < (int)(((c + 1) * p.batch) / C); ++b) {
-        if (own_len(p, b, false) == 0) {
+        if (own_len<kGroups>(p, b, false) == 0) {
           for (int i = lane; i < p.num_q_heads * D; i += 32)
             p.out[(int64_t)b * p.num_q_heads * D + i] = __float2bfloat16(0.f);
           if (p.lse)
@@ -420,12 +425,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (lane == 0) s_misc[0] = (int)n_tiles;
     // (the lengths' place is the loads' from here on)
-    if (lens) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (kGroups && lens) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   __syncthreads();
   n_tiles = s_misc[0];
   if (n_tiles == 0) {
-    if (warp == kProducerWarp) await_prefix(p);
+    if (kGroups && warp == kProducerWarp) await_prefix();
     return;
   }
 
@@ -503,18 +508,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int x = at + lane;
       my_own = my_page = 0;
       if (x < p.batch) {
-        my_own = own_len(p, x, false);
+        my_own = own_len<kGroups>(p, x, false);
         my_page = (clamp_len(p, __ldg(p.seq_lens + x), false) - my_own) / p.page_size;
       }
     };
     auto len_of = [&](int x) -> int {  // (x does not decrease)
-      if (!p.cu_groups) return own_len(p, x, false);
+      if (!kGroups) return own_len<kGroups>(p, x, false);
       if (x >= span_b0 + 32) look_up(x);
       return __shfl_sync(0xffffffffu, my_own, x - span_b0);
     };
-    if (p.cu_groups) look_up(b);
+    if (kGroups) look_up(b);
     int len = len_of(b);
-    int first_page = p.cu_groups ? __shfl_sync(0xffffffffu, my_page, b - span_b0) : 0;
+    int first_page = kGroups ? __shfl_sync(0xffffffffu, my_page, b - span_b0) : 0;
     int ntile = tiles_of<kTile>(len);
     int seg_first_t = t;
     // page ids (and scales) of 32 consecutive pages, one per lane
@@ -605,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         ti.valid = min(kTile, len - tok0);
         ti.flags = (first ? kSegFirst : 0) | (last ? kSegLast : 0) | hflags;
         // (with shared prefixes no unit is whole: its prefix part is to come)
-        if (last && seg_first_t == 0 && t == ntile - 1 && !p.cu_groups) ti.flags |= kUnitWhole;
+        if (last && seg_first_t == 0 && t == ntile - 1 && !kGroups) ti.flags |= kUnitWhole;
         if (first) {
           // once per unit: which CTAs share it, hence its partial slots
           const int64_t u = (int64_t)b * Hkv + g;
@@ -679,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             len = b < p.batch ? len_of(b) : 0;
           } while (b < p.batch && tiles_of<kTile>(len) == 0);
           if (b < p.batch) {
-            if (p.cu_groups) first_page = __shfl_sync(0xffffffffu, my_page, b - span_b0);
+            if (kGroups) first_page = __shfl_sync(0xffffffffu, my_page, b - span_b0);
             ntile = tiles_of<kTile>(len);
           }
         }
@@ -690,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t lo = issued > kStages ? issued - kStages : 0;
     for (int64_t k = lo; k < issued; ++k)
       mbar_wait(&full[k % kStages], (uint32_t)((k / kStages) & 1), p.flags);
-    await_prefix(p);
+    if (kGroups) await_prefix();
     return;
   }
 
@@ -1237,7 +1242,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const DecodeParams p)
   const int b = u / p.num_kv_heads;
   const int g = u - b * p.num_kv_heads;
   const int2 info = p.unit_info[u];
-  if (own_len(p, b, false) == 0) return;  // written by the decode kernel
+  if (clamp_len(p, __ldg(p.seq_lens + b), false) == 0) return;  // written by the decode kernel
   const int n = info.y;
   if (n <= 1) return;  // whole unit: written by the decode kernel
   constexpr int GD = G * D;
@@ -1324,12 +1329,15 @@ size_t decode_smem_bytes(int G) {
 
 template <int D, int kFmt, int kStages, int kSnap>
 cudaError_t decode_prepare(int G, int* ctas_per_sm) {
-  auto k = decode_kernel<D, kFmt, kStages, kSnap>;
+  auto k = decode_kernel<D, kFmt, kStages, kSnap, false>;
+  auto k_groups = decode_kernel<D, kFmt, kStages, kSnap, true>;
   const size_t smem = decode_smem_bytes<D, kFmt, kStages, kSnap>(G);
   // The attribute belongs to the instantiation, which serves every group
   // size: allow the largest footprint once, not the one of this call.
   const size_t most = decode_smem_bytes<D, kFmt, kStages, kSnap>(kMaxGroup);
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(k_groups, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e != cudaSuccess) return e;
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, k, kThreads, smem);
 }
@@ -1349,9 +1357,9 @@ cudaError_t decode_launch(const CUtensorMap& tk, const CUtensorMap& tv, const De
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_kernel<D, kFmt, kStages, kSnap>, tk, tv, p);
+    return cudaLaunchKernelEx(&cfg, decode_kernel<D, kFmt, kStages, kSnap, true>, tk, tv, p);
   }
-  decode_kernel<D, kFmt, kStages, kSnap><<<num_ctas, kThreads, smem, stream>>>(tk, tv, p);
+  decode_kernel<D, kFmt, kStages, kSnap, false><<<num_ctas, kThreads, smem, stream>>>(tk, tv, p);
   return cudaGetLastError();
 }
 
