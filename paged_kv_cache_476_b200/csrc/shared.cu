@@ -80,9 +80,10 @@ constexpr float kTiny = 1.17549435e-38f;       // smallest normal fp32
 constexpr float kSumUnit = 1.f / (1ull << 60);  // unit of l for quantised pools
 
 // Registers of the softmax, the load / product / scheduler and the converter
-// warps for quantised pools: 256 x 152 + 128 x 80 + 256 x 48 = 640 x 96, what
-// the block is launched with.
-constexpr int kSoftmaxRegs = 152, kIssueRegs = 80, kConvRegs = 48, kLaunchRegs = 96;
+// warps for quantised pools: 256 x 144 + 128 x 64 + 256 x 64 = 640 x 96, what
+// the block is launched with.  (152 / 80 / 48: 29 in place of 26 us for the FP4
+// prefixes of 48 rows, 168 / 64 / 40: 31; one-byte pools within 3 %.)
+constexpr int kSoftmaxRegs = 144, kIssueRegs = 64, kConvRegs = 64, kLaunchRegs = 96;
 static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs + 256 * kConvRegs <= 640 * kLaunchRegs, "");
 
 struct TileFacts {
