@@ -1044,8 +1044,8 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
 // add up the prefix partials of its G rows and the partials of the sequence's own
 // tokens.  The (m, l) of all parts come first, spread over the threads, and give
 // every part its weight 2^(m_i - M); the sum over the o_i then has no chain
-// through it: the warps take parts in turn, eight vectors in flight a lane, and
-// add up in shared memory.  Bound by its four trips to memory (7 us alone for 512
+// through it: a warp takes its share of the outputs, eight vectors in flight a
+// lane.  Bound by its four trips to memory (7 us alone for 512
 // units of three parts; 62 us with a chain through the parts).  Launched as a
 // programmatic dependent of the decode kernel, whose completion (and memory) it
 // awaits.
@@ -1060,17 +1060,15 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   constexpr int kUnits = kMergeThreads / kThreads;
   constexpr int kChunk = 2048 / G / kUnits;     // parts whose weights fit the shared array
   constexpr int kVecs = G * D / 4;              // float4 vectors of the unit's output
-  constexpr int kN = (kVecs + 31) / 32;         // of a lane
-  constexpr int kInFlight = kN >= 8 ? 1 : 8 / kN;  // parts a lane loads together
+  constexpr int kN = (kVecs / kW + 31) / 32;    // of a lane
+  constexpr int kInFlight = 8 / kN;             // parts a lane loads together
   __shared__ float s_w_all[kUnits][kChunk * G];
   __shared__ float s_red_all[kUnits][2][kW][G];
-  __shared__ float4 s_acc_all[kUnits][kW][kVecs];
   const DecodeParams& p = sp.d;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % kW;
   const int tid = threadIdx.x % kThreads, slot = threadIdx.x / kThreads;
   auto& s_w = s_w_all[slot];
   auto& s_red = s_red_all[slot];
-  auto& s_acc = s_acc_all[slot];
   auto unit_sync = [&]() {
     if constexpr (kW == 4)
       __syncthreads();
@@ -1153,6 +1151,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   float4 acc[kN];
 #pragma unroll
   for (int i = 0; i < kN; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int v0 = warp * (32 * kN) + lane;  // this lane's vectors: v0 + 32 j
   float L = 0.f;
   for (int c0 = 0; c0 < n; c0 += kChunk) {
     const int cn = min(n - c0, kChunk);
@@ -1164,7 +1163,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
       L += w * ml.y;
     }
     unit_sync();
-    for (int i0 = warp * kInFlight; i0 < cn; i0 += kW * kInFlight) {
+    for (int i0 = 0; i0 < cn; i0 += kInFlight) {
       float4 o[kInFlight][kN];
       float w[kInFlight][kN];
 #pragma unroll
@@ -1174,8 +1173,8 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
         const Place pl = pre ? place(i) : Place{own_row + (int64_t)(i - n_pre) * G, 0, 0};
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
-          const int v = lane + 32 * j;  // row v % G, dims 4 * (v / G)
-          w[k][j] = i0 + k < cn && (kVecs >= 32 || v < kVecs) ? s_w[(i0 + k) * G + v % G] : 0.f;
+          const int v = v0 + 32 * j;  // row v % G, dims 4 * (v / G)
+          w[k][j] = i0 + k < cn && v < kVecs ? s_w[(i0 + k) * G + v % G] : 0.f;
           o[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (w[k][j] != 0.f)
             o[k][j] = pre ? __ldcg(reinterpret_cast<const float4*>(sp.pre_o) + pl.first * (D / 4) +
@@ -1198,25 +1197,19 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
 #pragma unroll
   for (int o = G; o < 32; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   if (lane < G) s_red[1][warp][lane] = L;
-#pragma unroll
-  for (int j = 0; j < kN; ++j)
-    if (kVecs >= 32 || lane < kVecs) s_acc[warp][lane + 32 * j] = acc[j];
   unit_sync();
-  for (int v = tid; v < kVecs; v += kThreads) {
-    const int row = v % G;
-    float4 a = s_acc[0][v];
-    float l = s_red[1][0][row];
 #pragma unroll
-    for (int w = 1; w < kW; ++w) {
-      const float4 x = s_acc[w][v];
-      a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
-      l += s_red[1][w][row];
-    }
+  for (int j = 0; j < kN; ++j) {
+    const int v = v0 + 32 * j;
+    if (v >= kVecs) break;
+    const int row = v % G;  // (which is tid % G: M belongs to it)
+    float l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) l += s_red[1][w][row];
     const int64_t orow = (int64_t)b * p.num_q_heads + g * G + row;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2*>(p.out + orow * D + 4 * (v / G)) =
-        make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-    // (M belongs to row tid % G, which is v % G)
+    *reinterpret_cast<uint2*>(p.out + orow * D + 4 * (v / G)) = make_uint2(
+        pack_bf16(acc[j].x * inv, acc[j].y * inv), pack_bf16(acc[j].z * inv, acc[j].w * inv));
     if (p.lse && v < G)
       p.lse[orow] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
   }
