@@ -259,7 +259,10 @@ __global__ void __launch_bounds__(kRopeThreads, Shape<kFmt>::kBlocks) rope_kerne
   const int turns_all = __reduce_max_sync(0xffffffffu, rows);
   for (int r0 = 0; r0 < turns_all; r0 += kRows) {
     uint4 na[kRows], nb[kRows];
-    if (kAhead) load(r0 + kRows, na, nb);  // the next rows, while these are worked on
+    if (kAhead)
+      load(r0 + kRows, na, nb);  // the next rows, while these are worked on
+    else if (r0 > 0)
+      load(r0, ra, rb);
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const bool row_live = live && r0 + r < rows;

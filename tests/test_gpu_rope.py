@@ -372,3 +372,41 @@ def test_refusals_from_python(pkv):
         with pytest.raises(ValueError):
             pkv.paged_kv_append_rope(pool.cache, rope, *good, **kw)
     assert int(pool.flags) == 0
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 32, 8), (128, 13, 5), (64, 21, 3), (128, 9, 0)])
+@pytest.mark.parametrize("T", [150, 700, 1500, 3100, 9001])
+def test_every_number_of_rows_an_item(pkv, D, Hq, Hkv, T):
+    """Batches on both sides of where an item takes two, four and eight rows, with head
+    counts that leave items short."""
+    x = torch.randn(T, Hq + Hkv, D, generator=_gen(T)).bfloat16().cuda()
+    q, k = x[:, :Hq], x[:, Hq:] if Hkv else None
+    for inter, norm in ((False, True), (True, False)):
+        rope = _rope(pkv, D, D, inter, norm)
+        pos = np.random.default_rng(T).integers(0, 4096, T).astype(np.int32)
+        qo, ko = pkv.pkv_qk_norm_rope(rope, q, k, torch.from_numpy(pos).cuda())
+        assert_bf16_rows(qo, *_expect(q, pos, rope, D, "q"))
+        if Hkv:
+            assert_bf16_rows(ko, *_expect(k, pos, rope, D, "k"))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,Hq,Hkv", [(400, 32, 8), (900, 24, 5), (2200, 16, 8), (5000, 8, 3)])
+def test_large_appends(pkv, fmt, T, Hq, Hkv):
+    """The same for the append: pools and queries against a call for each few tokens."""
+    D, P = 128, 64
+    q, k, v = _fused(T, Hq, Hkv, D, T)
+    rope = _rope(pkv, D, 64, False, True, most=8192)
+    n = -(-T // P)
+    table = torch.randperm(n, generator=_gen(1)).int()[None].cuda()
+    ints = lambda *a: torch.tensor(a, dtype=torch.int32).cuda()
+    pools = [_Pool(pkv, fmt, n, Hkv, P, D) for _ in range(2)]
+    whole = pkv.paged_kv_append_rope(pools[0].cache, rope, table, ints(0), ints(0, T), k, v, q=q)
+    for at in range(0, T, 16):  # (one row an item)
+        m = min(16, T - at)
+        part = pkv.paged_kv_append_rope(pools[1].cache, rope, table, ints(at), ints(0, m),
+                                        k[at:at + m], v[at:at + m], q=q[at:at + m])
+        assert torch.equal(whole[at:at + m], part)
+    assert torch.equal(pools[0].k, pools[1].k) and torch.equal(pools[0].v, pools[1].v)
+    z, mag = _expect(q, np.arange(T), rope, 64, "q")
+    assert_bf16_rows(whole, z, mag)
