@@ -33,18 +33,13 @@ using pf::fma2;
 using pf::mul2;
 
 constexpr int kRopeThreads = 256;
-// Blocks of an SM (80 or 128 registers a thread), rows a lane works on together,
-// and whether it loads the next ones meanwhile.  Measured (4,400 GB/s and up):
-// 16,384 tokens of 32 / 8 heads 65 us at (3, 2, no), 65 at (2, 2, yes), 79 at (2,
-// 1, yes); appends in bf16 of 8,900 tokens 46, 52, 61; in E4M3, where the codes'
-// arithmetic spills at 80 registers, of 740 tokens of 64 / 8 heads 22, 17, 18.
-template <int kFmt>
-struct Shape {
-  static constexpr bool kSpare = kFmt > 0;  // quantised pool
-  static constexpr int kBlocks = kSpare ? 2 : 3;
-  static constexpr int kRows = 2;
-  static constexpr bool kAhead = kSpare;
-};
+// Blocks of an SM (128 registers a thread) and rows a lane works on together, the
+// next ones loading meanwhile, in items of more than one row.  Measured (us a call:
+// 16,384 tokens of 32 / 8 heads; bf16 append of 8,900 tokens): 2 blocks of 2 rows 70
+// and 55, without the load ahead 80 and 68; 3 blocks of 1 row 70 and 60, of 2 rows
+// 90 and 72 (spills), without the load ahead 74 and 62; 2 blocks of 4 rows 77 and 65.
+constexpr int kRopeBlocks = 2;
+constexpr int kRopeRows = 2;
 
 __device__ __forceinline__ float2 bf16_pair(uint32_t w) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
@@ -122,8 +117,8 @@ __device__ __forceinline__ float amax8(const float* x) {
 }
 
 // kFmt < 0: no cache, rotated k to k_out.
-template <int D, int kFmt, int kRows, bool kAhead, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads, Shape<kFmt>::kBlocks) rope_kernel(const RopeParams p) {
+template <int D, int kFmt, int kRows, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kernel(const RopeParams p) {
   constexpr bool kAppend = kFmt >= 0;
   constexpr int L = D / 16;
   const int lane = threadIdx.x & 31;
@@ -259,10 +254,7 @@ __global__ void __launch_bounds__(kRopeThreads, Shape<kFmt>::kBlocks) rope_kerne
   const int turns_all = __reduce_max_sync(0xffffffffu, rows);
   for (int r0 = 0; r0 < turns_all; r0 += kRows) {
     uint4 na[kRows], nb[kRows];
-    if (kAhead)
-      load(r0 + kRows, na, nb);  // the next rows, while these are worked on
-    else if (r0 > 0)
-      load(r0, ra, rb);
+    load(r0 + kRows, na, nb);  // the next rows (if any), while these are worked on
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const bool row_live = live && r0 + r < rows;
@@ -355,23 +347,21 @@ __global__ void __launch_bounds__(kRopeThreads, Shape<kFmt>::kBlocks) rope_kerne
         }
       }
     }
-    if (kAhead) {
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) ra[r] = na[r], rb[r] = nb[r];
-    }
+    for (int r = 0; r < kRows; ++r) ra[r] = na[r], rb[r] = nb[r];
   }
 }
 
-template <int D, int kFmt, int kRows, bool kAhead>
+template <int D, int kFmt, int kRows>
 cudaError_t rope_launch(const RopeParams& p, int64_t items, cudaStream_t stream) {
   const int64_t blocks = (items * (D / 16) + kRopeThreads - 1) / kRopeThreads;
   if (blocks == 0) return cudaSuccess;
   if (blocks * kRopeThreads > INT32_MAX) return cudaErrorInvalidConfiguration;
   if (p.interleaved)
-    rope_kernel<D, kFmt, kRows, kAhead, true>
+    rope_kernel<D, kFmt, kRows, true>
         <<<(unsigned)blocks, kRopeThreads, 0, stream>>>(p);
   else
-    rope_kernel<D, kFmt, kRows, kAhead, false>
+    rope_kernel<D, kFmt, kRows, false>
         <<<(unsigned)blocks, kRopeThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
@@ -390,12 +380,11 @@ cudaError_t rope_run(RopeParams p, int head_dim, int num_sms, cudaStream_t strea
   while (per > 1 && items(per) < enough) per /= 2;
   p.rows_per_item = per;
   const int64_t n = items(per);
-  using Sh = Shape<kFmt>;
   if (head_dim == 128)
-    return per > 1 ? rope_launch<128, kFmt, Sh::kRows, Sh::kAhead>(p, n, stream)
-                   : rope_launch<128, kFmt, 1, false>(p, n, stream);
-  return per > 1 ? rope_launch<64, kFmt, Sh::kRows, Sh::kAhead>(p, n, stream)
-                 : rope_launch<64, kFmt, 1, false>(p, n, stream);
+    return per > 1 ? rope_launch<128, kFmt, kRopeRows>(p, n, stream)
+                   : rope_launch<128, kFmt, 1>(p, n, stream);
+  return per > 1 ? rope_launch<64, kFmt, kRopeRows>(p, n, stream)
+                 : rope_launch<64, kFmt, 1>(p, n, stream);
 }
 
 }  // namespace
