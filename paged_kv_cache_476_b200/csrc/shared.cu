@@ -14,8 +14,8 @@
 //  * Bound: HBM bytes of the prefix for one Q tile of bf16 (1.4 us a 128-key tile
 //    and SM at head_dim 128: the SM's share); the cycle of a slot, its softmax, the
 //    products and the hand-offs between them, for two (2.35 us a tile; 3.0 of
-//    quantised pools); the converters for one Q tile of quantised pools (1.45 us,
-//    FP4 1.75).  16 sequences behind 65,536 bf16 tokens of 8 kv heads: 54 us, 4.9
+//    quantised pools); the converters for one Q tile of quantised pools (about 1.4
+//    us, FP4 1.6).  16 sequences behind 65,536 bf16 tokens of 8 kv heads: 54 us, 4.9
 //    TB/s, of which 6 us pass before the first tile has landed.
 //  * Items.  A group's rows of one kv head are cut into pairs of 128-row Q
 //    tiles, A and B.  An item is (group, kv head, pair) over the prefix's
@@ -267,7 +267,7 @@ __device__ int first_holder(const DecodeParams& p, const GroupWork& w, int lane)
 // 2688]), laid out as TMA lays out 16-bit tiles.  Half h (64 rows, one page) is
 // written as zeros unless bit h of `live` is set.  A thread makes 16-byte
 // chunks of one column, eight threads a 128-byte line, so that neither its loads
-// nor its stores meet in a bank; all loads of a half come before its stores.
+// nor its stores meet in a bank; four units' loads come before their stores.
 template <int D, int kFmt>
 __device__ __forceinline__ void convert_codes(uint32_t src, uint32_t dst, int t, int live) {
   constexpr int kCols = D / 8;                  // 8-value columns of a row
