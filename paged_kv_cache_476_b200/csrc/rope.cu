@@ -32,13 +32,14 @@ namespace {
 using pf::fma2;
 using pf::mul2;
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 64;
 // Blocks of an SM (128 registers a thread) and rows a lane works on together, the
 // next ones loading meanwhile, in items of more than one row.  Measured (us a call:
-// 16,384 tokens of 32 / 8 heads; bf16 append of 8,900 tokens): 2 blocks of 2 rows 70
-// and 55, without the load ahead 80 and 68; 3 blocks of 1 row 70 and 60, of 2 rows
-// 90 and 72 (spills), without the load ahead 74 and 62; 2 blocks of 4 rows 77 and 65.
-constexpr int kRopeBlocks = 2;
+// 16,384 tokens of 32 / 8 heads; bf16 append of 8,900 tokens), in 512 threads an SM:
+// 66 and 53 in blocks of 64 threads, 67.6 and 53 of 128, 70 and 55 of 256 (whose last
+// warps hold the others' places); of 256, without the load ahead 80 and 68, with 4
+// rows 77 and 65; in 768 threads 1 row 70 and 60, 2 rows 90 and 72 (spills).
+constexpr int kRopeBlocks = 8;
 constexpr int kRopeRows = 2;
 
 __device__ __forceinline__ float2 bf16_pair(uint32_t w) {
@@ -373,9 +374,9 @@ cudaError_t rope_run(RopeParams p, int head_dim, int num_sms, cudaStream_t strea
     const int nq = (p.num_q_heads + per - 1) / per, nk = (p.num_kv_heads + per - 1) / per;
     return (int64_t)p.tokens * (nq + (kFmt >= 0 ? 2 : 1) * nk);
   };
-  // As many rows an item as leave every SM a block and a half: the way to the
-  // first product costs a lane as much as two rows.
-  const int64_t enough = (int64_t)num_sms * kRopeThreads * 3 / 2 / (head_dim / 16);
+  // As many rows an item as leave every SM 384 threads: the way to the first product
+  // costs a lane as much as two rows.
+  const int64_t enough = (int64_t)num_sms * 384 / (head_dim / 16);
   int per = 8;
   while (per > 1 && items(per) < enough) per /= 2;
   p.rows_per_item = per;
