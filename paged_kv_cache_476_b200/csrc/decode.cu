@@ -29,7 +29,8 @@
 //    against a two-term fixed-point Q; E4M3 K and all V codes convert
 //    exactly to f16 in registers after ldmatrix (FP4 times its E4M3 block
 //    scales).  The per-(page, head) scales fold into the scores (K) and
-//    into P (V).
+//    into P (V), which is held in a power-of-two unit of the largest V scale
+//    so far so that f16 keeps its bits for every scale.
 //  * Every wait is bounded; a bad page id or length is skipped and flagged.
 #include <type_traits>
 
@@ -102,7 +103,7 @@ struct Layout {
 // one per consumer warp (4), or one per warp pair (2) where that buys a
 // deeper ring.
 struct SmemPlan {
-  uint32_t q, red_o, red_m, red_l, bars, info, misc, total;
+  uint32_t q, red_o, red_m, red_l, red_u, bars, info, misc, total;
 };
 
 __host__ __device__ inline uint32_t align_up(uint32_t x, uint32_t a) { return (x + a - 1) / a * a; }
@@ -121,6 +122,8 @@ __host__ __device__ inline SmemPlan smem_plan(int G) {
   o += kSnap * G * 4;
   s.red_l = o;
   o += kSnap * G * 4;
+  s.red_u = o;
+  o += quant(kFmt) ? kSnap * 4 : 0;
   o = align_up(o, 8);
   s.bars = o;
   o += (2 * kStages + 3) * 8;
@@ -161,6 +164,22 @@ __device__ __forceinline__ uint32_t tile_at(uint32_t base, LaneTile lt, int ce) 
   constexpr int kChunksPerBox = kBoxRowB / 16;
   return base + (ce / kChunksPerBox) * (kRows * kBoxRowB) + lt.a +
          (((uint32_t)(ce % kChunksPerBox) << 4) ^ lt.x);
+}
+
+// Quantised pools: the power of two that P times the V scale is held in, vs * unit
+// in [2^14, 2^15) (below for vs < 2^-111, with the unit at its limit), so that with
+// P <= 1 the f16 value stays in range and keeps its 11 bits down to 2^-28 of the
+// largest.  In place of P * vs itself, which has a fixed step of 2^-24 below 2^-14:
+// a page of E4M3 values of N(0, 1) has vs = 0.01, and weights below 2^-18 of the
+// largest were lost to the output while the sum kept them.  Two units differ by at
+// most 2^126, so that their ratio is a normal number.
+constexpr int kMaxUnit = 125;
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ float v_unit(float vs) {
+  return pow2(min(kMaxUnit, 14 + 127 - (int)(__float_as_uint(vs) >> 23)));
+}
+__device__ __forceinline__ float pow2_ratio(float a, float b) {
+  return __uint_as_float(__float_as_uint(a) - __float_as_uint(b) + 0x3f800000u);
 }
 
 // CTA (of C <= T over T virtual tiles) whose range [c*T/C, (c+1)*T/C) holds
@@ -333,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* red_o = reinterpret_cast<float*>(smem + sp.red_o);
   float* red_m = reinterpret_cast<float*>(smem + sp.red_m);
   float* red_l = reinterpret_cast<float*>(smem + sp.red_l);
+  float* red_u = reinterpret_cast<float*>(smem + sp.red_u);  // units of the snapshots' o
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + sp.bars);
   uint64_t* empty = full + kStages;
   uint64_t* red_full = empty + kStages;   // consumers -> flush warp: the kSnap snapshots are ready
@@ -453,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const float mw = red_m[w * G + r];
           sc[w] = (M == -INFINITY || mw == -INFINITY) ? 0.f : fast_exp2(mw - M);
           den += sc[w] * red_l[w * G + r];
+          if constexpr (quant(kFmt)) sc[w] *= pow2_ratio(1.f, red_u[w]);
         }
         const int64_t orow = (int64_t)fd.b * p.num_q_heads + fd.g * G + r;
         const float inv = den > 0.f ? 1.f / den : 0.f;
@@ -721,6 +742,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // running max and partial sum of heads 2*tid4 and 2*tid4 + 1 (the O^T
   // columns of this thread)
   float m_run[2] = {-INFINITY, -INFINITY}, l_part[2] = {0.f, 0.f};
+  float unit = pow2(kMaxUnit);  // quantised: ot holds the output times this
   float qk_mul = p.scale_log2;  // multiplier of head gid's raw scores into log2 units
   float hmul[2] = {p.scale_log2, p.scale_log2};  // the same for heads 2*tid4, 2*tid4 + 1
   // K rows a lane addresses in ldmatrix.x4: matrices (tokens 0-7, chunk ce),
@@ -752,6 +774,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (t_flags & kSegFirst) {
       m_run[0] = m_run[1] = -INFINITY;
       l_part[0] = l_part[1] = 0.f;
+      unit = pow2(kMaxUnit);
 #pragma unroll
       for (int m = 0; m < D / 16; ++m) ot[m][0] = ot[m][1] = ot[m][2] = ot[m][3] = 0.f;
       if constexpr (!quant(kFmt)) {
@@ -978,14 +1001,25 @@ __global__ void __launch_bounds__(kThreads, 2)
       m_run[0] = mn0;
       m_run[1] = mn1;
       // The factors belong to this thread's own O^T columns.  Once the
-      // running max settles (most tiles), no head's factor moves.
-      if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
+      // running max and the unit settle (most tiles), no head's factor moves.
+      float f0 = al0, f1 = al1, p_mul = 1.f;
+      if constexpr (quant(kFmt)) {
+        p_mul = t_vs * unit;  // (the warp's rows lie in one page)
+        if (p_mul >= 32768.f) {
+          const float u = v_unit(t_vs);
+          f0 *= pow2_ratio(u, unit);
+          f1 *= pow2_ratio(u, unit);
+          unit = u;
+          p_mul = t_vs * u;
+        }
+      }
+      if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
 #pragma unroll
         for (int m = 0; m < D / 16; ++m) {
-          ot[m][0] *= al0;
-          ot[m][1] *= al1;
-          ot[m][2] *= al0;
-          ot[m][3] *= al1;
+          ot[m][0] *= f0;
+          ot[m][1] *= f1;
+          ot[m][2] *= f0;
+          ot[m][3] *= f1;
         }
       }
       // ---- O^T += V^T P^T over my tokens (P^T: a transpose of P packed) ----
@@ -1005,8 +1039,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             q0 = pack_bf16(pr[hv][0], pr[hv][1]);
             q1 = pack_bf16(pr[hv][2], pr[hv][3]);
           } else {
-            q0 = pack_f16(pr[hv][0] * t_vs, pr[hv][1] * t_vs);
-            q1 = pack_f16(pr[hv][2] * t_vs, pr[hv][3] * t_vs);
+            q0 = pack_f16(pr[hv][0] * p_mul, pr[hv][1] * p_mul);
+            q1 = pack_f16(pr[hv][2] * p_mul, pr[hv][3] * p_mul);
           }
           const uint32_t pa0 = movmatrix_t(q0);
           const uint32_t pa2 = movmatrix_t(q1);
@@ -1143,6 +1177,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       };
       if (kSnap == kConsumerWarps || warp >= kSnap) {
         if (nflush > 0 && !mbar_wait(red_empty, (uint32_t)((nflush - 1) & 1), p.flags)) return;
+        if (quant(kFmt) && lane == 0) red_u[slot] = unit;
         if (gid == 0) {
           if (h0 < G) {
             red_m[slot * G + h0] = m_run[0];
@@ -1189,7 +1224,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           sb[k] = mp == -INFINITY ? 0.f : fast_exp2(mp - M[k]);
           l_new[k] = sa[k] * l_h[k] + sb[k] * lp;
         }
-        const float a_lo = sa[0], a_hi = sa[1], b_lo = sb[0], b_hi = sb[1];
+        float a_lo = sa[0], a_hi = sa[1], b_lo = sb[0], b_hi = sb[1];
+        if constexpr (quant(kFmt)) {  // both sides' o to the smaller unit
+          const float up = red_u[slot], u = fminf(unit, up);
+          const float ra = pow2_ratio(u, unit), rb = pow2_ratio(u, up);
+          a_lo *= ra, a_hi *= ra, b_lo *= rb, b_hi *= rb;
+          unit = u;
+        }
         float* r0 = so + h0 * kRedRow;
         float* r1 = so + h1 * kRedRow;
 #pragma unroll
@@ -1205,6 +1246,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         __syncwarp();  // every lane has read the partner's (m, l)
+        if (quant(kFmt) && lane == 0) red_u[slot] = unit;
         if (gid == 0) {
           if (h0 < G) {
             red_m[slot * G + h0] = M[0];
