@@ -78,6 +78,11 @@ constexpr int kPairRows = 2 * kRows;
 constexpr int kMaxSegments = 1 << 16;     // more than any GPU has SMs
 constexpr float kTiny = 1.17549435e-38f;       // smallest normal fp32
 constexpr float kSumUnit = 1.f / (1ull << 60);  // unit of l for quantised pools
+// A V scale more than 2^64 below the segment's largest so far (a page of zeros may
+// have the smallest float) would take P, and with it the row sum's share, out of
+// fp32's range.  Such a block's weights are held as if its scale were 2^64 below,
+// for the sum; its values, 2^-64 of the others', are left out.
+constexpr float kScaleReach = 64.f;
 
 // Registers of the softmax, the load / product / scheduler and the converter
 // warps for quantised pools: 256 x 144 + 128 x 64 + 256 x 64 = 640 x 96, what
@@ -86,8 +91,9 @@ constexpr float kSumUnit = 1.f / (1ull << 60);  // unit of l for quantised pools
 constexpr int kSoftmaxRegs = 144, kIssueRegs = 64, kConvRegs = 64, kLaunchRegs = 96;
 static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs + 256 * kConvRegs <= 640 * kLaunchRegs, "");
 
+constexpr int kNoValue = 4;
 struct TileFacts {
-  int32_t bad;  // bit per 64-key block: rejected page
+  int32_t bad;  // bit per 64-key block: rejected page; times kNoValue: for the sum alone
   float ks[2];  // K scales of the blocks' pages
   float lv[2];  // log2 of the V scales
   float iv[2];  // kSumUnit over the V scales
@@ -572,7 +578,17 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         auto set_max = [&](float mt) -> float {
           const bool need = mt > m_ref + 8.f;
           const float m_new = need ? mt : m_ref;
-          if (q >= 1 && need) alpha = fast_exp2(m_ref - m_new);
+          if (q >= 1 && need) {
+            if constexpr (quant(kFmt)) {
+              // (the sum reaches from 2^-75 to 2^94 and takes a factor below fp32's range)
+              const float half = fast_exp2(0.5f * (m_ref - m_new));
+              alpha = half * half;
+              l = (l * half) * half;
+            } else {
+              alpha = fast_exp2(m_ref - m_new);
+              l *= alpha;
+            }
+          }
           m_ref = m_new;
           return m_ref == -INFINITY ? 0.f : m_ref;
         };
@@ -618,7 +634,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           }
         }
         if (__any_sync(0xffffffffu, alpha != 1.f)) rescale_o<D>(tmem + lane_base + colO, alpha);
-        l = l * alpha + rs;
+        l += rs;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -763,6 +779,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
                            key0 % p.page_size);
           my_live = 1;
         };
+        float top = -INFINITY;  // log2 of the segment's largest V scale so far
         for (int i = 0; i < sg.n; ++i, ++j) {
           if ((i & 15) == 0) lookup(i);
           TileFacts tf;
@@ -779,7 +796,18 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
               tf.ks[sb] = __shfl_sync(0xffffffffu, my_ks, from);
               tf.lv[sb] = __shfl_sync(0xffffffffu, my_lv, from);
               tf.iv[sb] = __shfl_sync(0xffffffffu, my_iv, from);
+              if ((live >> sb) & 1) top = fmaxf(top, tf.lv[sb]);
             }
+          }
+          if constexpr (quant(kFmt)) {
+            const float least = top - kScaleReach;
+#pragma unroll
+            for (int sb = 0; sb < 2; ++sb)
+              if (((live >> sb) & 1) && tf.lv[sb] < least) {
+                tf.bad |= kNoValue << sb;
+                tf.lv[sb] = least;
+                tf.iv[sb] = kSumUnit * fast_exp2(-least);
+              }
           }
           auto load = [&](const CUtensorMap* map, const uint8_t* blocks, uint8_t* dst,
                           uint64_t* bar) {
@@ -1010,7 +1038,8 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
             break;
           }
           // (pages, and with them the prefix, end on 64 keys)
-          live = ~ct.facts[j % kFactsRing].bad &
+          const int bad = ct.facts[j % kFactsRing].bad;
+          live = ~(v ? bad | bad / kNoValue : bad) &
                  ((sg.tile0 + i) * kKeys + 64 < sg.prefix ? 3 : 1);
         }
         const uint8_t* to = v ? v_made(out.slot) : sconv + out.slot * Sm::kTileB;
@@ -1158,9 +1187,11 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
     if (c0 > 0) unit_sync();  // the last chunk's weights have been used
     for (int i = my_part; i < cn; i += kStep) {
       const float2 ml = c0 + i == my_part ? my_ml : ml_of(c0 + i, my_row);
-      const float w = ml.y != 0.f ? fast_exp2(ml.x - M) : 0.f;
-      s_w[i * G + my_row] = w;
-      L += w * ml.y;
+      // in two factors: the sums of quantised pools' parts reach from 2^-75 to 2^94, and
+      // where the weight is below fp32's range the weighted sum is not
+      const float half = ml.y != 0.f ? fast_exp2(0.5f * (ml.x - M)) : 0.f;
+      s_w[i * G + my_row] = half * half;
+      L += (half * ml.y) * half;
     }
     unit_sync();
     for (int i0 = 0; i0 < cn; i0 += kInFlight) {

@@ -93,3 +93,27 @@ def test_long_tail_behind_one_token(pkv, fmt):
     b.q.zero_()
     b.q[..., 0] = 14 * 0.693 / b.scale / top
     _both(pkv, b, num_ctas=1)  # one segment: all weights relative to that token's
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("zeros", [[0], [3], [9], [0, 1, 2, 3], [5, 6, 7, 8, 9], [0, 2, 4, 6, 8],
+                                   list(range(10))])
+@pytest.mark.parametrize("tiny,other", [(2.0 ** -126, 1.0), (1e-42, 1.0), (2.0 ** -126, 2.0 ** 18),
+                                        (2.0 ** -80, 2.0 ** 18)])
+def test_pages_of_zeros(pkv, fmt, zeros, tiny, other):
+    """Pages whose V is 0 and whose scale is the smallest there is still weigh in the sum."""
+    b = Batch([640, 700, 833, 2000], [0, 4], [640], 2, 4, 128, 64, fmt, seed=3)
+    _scale_v(b, torch.full_like(b.scales[1], other))
+    for j in zeros:
+        pid = int(b.table[0, j])
+        b.scales[1][pid] = tiny
+        b.values[1][pid] = 0
+        if fmt == "nvfp4":
+            n = 2 * 64 * 128 // 2  # code bytes of a page
+            b.pools[1][pid * n:(pid + 1) * n] = 0
+        else:
+            b.pools[1][pid] = 0
+    _both(pkv, b)
+    # one part alone: a prefix of these pages only, whatever the own tokens' scales are
+    b.lens = [640] * 4
+    _both(pkv, b)
