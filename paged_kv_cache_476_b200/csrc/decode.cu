@@ -166,22 +166,6 @@ __device__ __forceinline__ uint32_t tile_at(uint32_t base, LaneTile lt, int ce) 
          (((uint32_t)(ce % kChunksPerBox) << 4) ^ lt.x);
 }
 
-// Quantised pools: the power of two that P times the V scale is held in, vs * unit
-// in [2^14, 2^15) (below for vs < 2^-111, with the unit at its limit), so that with
-// P <= 1 the f16 value stays in range and keeps its 11 bits down to 2^-28 of the
-// largest.  In place of P * vs itself, which has a fixed step of 2^-24 below 2^-14:
-// a page of E4M3 values of N(0, 1) has vs = 0.01, and weights below 2^-18 of the
-// largest were lost to the output while the sum kept them.  Two units differ by at
-// most 2^126, so that their ratio is a normal number.
-constexpr int kMaxUnit = 125;
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-__device__ __forceinline__ float v_unit(float vs) {
-  return pow2(min(kMaxUnit, 14 + 127 - (int)(__float_as_uint(vs) >> 23)));
-}
-__device__ __forceinline__ float pow2_ratio(float a, float b) {
-  return __uint_as_float(__float_as_uint(a) - __float_as_uint(b) + 0x3f800000u);
-}
-
 // CTA (of C <= T over T virtual tiles) whose range [c*T/C, (c+1)*T/C) holds
 // virtual tile x.  With C <= T every range is non-empty.
 __device__ __forceinline__ int64_t cta_of(int64_t x, int64_t C, int64_t T) {

@@ -98,10 +98,12 @@ struct Smem {
 };
 
 // Per-KV-tile facts the producer passes on: rejected 64-key blocks and the
-// E4M3 scales of the (up to two) pages of the tile.
+// scales of the (up to two) pages of the tile, V's times the power of two that O
+// is held in (v_unit), and that unit's change over the tile before.
 struct TileFacts {
   int32_t bad;
   float ks[2], vs[2];
+  float unit, change;
 };
 constexpr int kFactsRing = 4;
 
@@ -403,7 +405,21 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           }
         }
       };
+      float unit = pow2(kMaxUnit);
+      auto to_unit = [&](Lookup& lk, bool first) {  // (tiles in turn)
+        lk.tf.unit = lk.tf.change = 1.f;
+        if constexpr (quant(kFmt)) {
+          const float was = unit;
+          const float top = fmaxf(lk.live & 1 ? lk.tf.vs[0] : 0.f, lk.live & 2 ? lk.tf.vs[1] : 0.f);
+          if (top * unit >= 32768.f) unit = v_unit(top);
+          if (!first) lk.tf.change = pow2_ratio(unit, was);
+          lk.tf.unit = unit;
+          lk.tf.vs[0] *= unit;
+          lk.tf.vs[1] *= unit;
+        }
+      };
       Lookup cur = lookup(0);
+      to_unit(cur, true);
       for (int j = 0; j < n_kv; ++j) {
         const int st = j % kStages;
         const uint32_t ph = (uint32_t)((j / kStages - 1) & 1);
@@ -417,7 +433,10 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         load(&tmap_k, p.k_blocks, kd, &k_full[st], cur);
         if (j >= kStages && !mbar_wait(&v_empty[st], ph, p.flags)) break;
         load(&tmap_v, p.v_blocks, vd, &v_full[st], cur);
-        if (j + 1 < n_kv) cur = lookup(j + 1);  // ahead of the next slot wait
+        if (j + 1 < n_kv) {  // ahead of the next slot wait
+          cur = lookup(j + 1);
+          to_unit(cur, false);
+        }
       }
     }
   } else if (quant(kFmt) && warp >= kConvWarp0) {
@@ -582,7 +601,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       const bool row_ok = t_local < n;
       const int32_t p_min = L - n + q0x;
       const int32_t pos = row_ok ? L - n + t_local : L - n + min(q0x + TQ, n) - 1;
-      float m_ref = -INFINITY, l = 0.f;
+      float m_ref = -INFINITY, l = 0.f, unit = 1.f;
       bool ok = true;
       for (int j = 0; j < nkx; ++j) {
         if (!mbar_wait(&s_full[x], (uint32_t)(j & 1), p.flags)) { ok = false; break; }
@@ -608,8 +627,8 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         // general way.)
         const bool plain = !diag && tf.bad == 0 && mul0 > 0.f && mul1 > 0.f;
         // Raise the reference max to the tile max mt when needed: lazily (p
-        // <= 2^8) for bf16; for E4M3 at every increase, so that p * v_scale
-        // <= 2^15 fits the f16 P.  Returns the max to subtract (0 while a row
+        // <= 2^8) for bf16; for quantised pools at every increase, so that p
+        // times the V scale in O's unit, below 2^15, fits the f16 P.  Returns the max to subtract (0 while a row
         // has seen no key, so that its p are 0).  O is rescaled by alpha
         // after P is written (the registers of S are free by then): S(j) done
         // implies every earlier MMA is done, PV(j-1) included, and PV(j)
@@ -653,7 +672,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
             tmem_ld32(tmem + lane_base + colS + cb + 32, sv + 32);
             tmem_wait_ld();
             const float mul = cb < 64 ? mul0 : mul1;
-            // quantised pools: the V scales ride on P
+            // quantised pools: the V scales (in O's unit) ride on P
             const float vsc = quant(kFmt) ? (cb < 64 ? tf.vs[0] : tf.vs[1]) : 1.f;
             uint32_t pk[32];
             // (two loops rather than a branch per element, which the compiler
@@ -689,8 +708,12 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
             tmem_st16(tmem + lane_base + colS + cb / 2 + 16, pk + 16);
           }
         }
-        if (__any_sync(0xffffffffu, alpha != 1.f)) rescale_o<D>(tmem + lane_base + colO, alpha);
         l = l * alpha + rs;
+        if constexpr (quant(kFmt)) {
+          alpha *= tf.change;
+          unit = tf.unit;
+        }
+        if (__any_sync(0xffffffffu, alpha != 1.f)) rescale_o<D>(tmem + lane_base + colO, alpha);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -701,6 +724,7 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           mbar_wait(&o_bar[x], (uint32_t)((nkx - 1) & 1), p.flags)) {
         tc_fence_after();
         const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float un = pow2_ratio(1.f, unit);  // (not folded into inv, which may be too small)
         const int64_t qrow = (int64_t)q_begin + t_local;
         const int h = g * G + (r % G);
         __nv_bfloat16* dst = p.out + (qrow * p.num_q_heads + h) * D;
@@ -710,6 +734,10 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           tmem_ld32(tmem + lane_base + colO + c, o);
           tmem_wait_ld();
           if (row_ok) {
+            if constexpr (quant(kFmt)) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= un;
+            }
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
               uint4 v;

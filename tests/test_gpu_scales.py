@@ -117,3 +117,24 @@ def test_pages_of_zeros(pkv, fmt, zeros, tiny, other):
     # one part alone: a prefix of these pages only, whatever the own tokens' scales are
     b.lens = [640] * 4
     _both(pkv, b)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D,Hkv,G,page", [(128, 2, 4, 64), (64, 3, 1, 128), (128, 1, 8, 128)])
+@pytest.mark.parametrize("shift,spread", [(0, 30), (-20, 0), (-60, 4), (-100, 2)])
+@pytest.mark.parametrize("L,n", [(700, 300), (65, 65), (1000, 1)])
+def test_prefill_with_v_scales_far_from_one(pkv, fmt, D, Hkv, G, page, shift, spread, L, n):
+    b = Batch([L], [0], [], Hkv, G, D, page, fmt, seed=6)
+    g = torch.Generator().manual_seed(shift + G)
+    r = 2.0 ** (torch.randint(0, spread + 1, b.scales[1].shape, generator=g).float()
+                - spread + shift)
+    _scale_v(b, r.to(b.q.device))
+    cache = b.cache(pkv)
+    q = torch.randn(n, Hkv * G, D, generator=g).bfloat16().cuda()
+    got = pkv.paged_prefill_chunk_attention(cache, q, b.ints([0, n]), b.table, b.ints([L]), n,
+                                            b.scale)
+    assert int(b.flags) == 0
+    # each query as a sequence of its own, of the tokens up to it
+    rows = _strict(b)
+    rows.q, rows.lens, rows.table = q, list(range(L - n + 1, L + 1)), b.table.expand(n, -1)
+    assert_exact(got, rows)
