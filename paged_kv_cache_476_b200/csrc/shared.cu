@@ -987,8 +987,10 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
         steps0 += (nsteps + 1) >> 1;
         steps1 += nsteps >> 1;
       }
-      // every MMA this thread issued must finish before TMEM is released
-      if (lane == 0) tc_commit(&ct.done);
+      // every product must finish before TMEM is released, also after a wait that gave
+      // up: the commit is the elected thread's, which issued them
+      __syncwarp();
+      if (elect_one()) tc_commit(&ct.done);
       __syncwarp();
     }
   } else if constexpr (quant(kFmt)) {
