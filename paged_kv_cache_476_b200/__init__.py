@@ -191,21 +191,6 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 
 
-def _load_binding():
-    """The CPython module of the rotation and shared-prefix calls, on this library."""
-    try:
-        from . import _binding
-    except ImportError as e:
-        raise ImportError(f"{_PKG}/_binding.so is missing or stale: build it with `python "
-                          "paged_kv_cache_476_b200/build.py`") from e
-    _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        _lib.pkv_qk_norm_rope, _lib.paged_kv_append_rope, _lib.paged_decode_attention_shared)))
-    return _binding
-
-
-_binding = _load_binding()
-
-
 def lib() -> ctypes.CDLL:
     return _lib
 
@@ -218,6 +203,22 @@ class PagedKVError(RuntimeError):
     def __init__(self, what: str, status: int):
         super().__init__(f"{what} failed: {pkv_status_string(status)} (status {status})")
         self.status = status
+
+
+def _load_binding():
+    """The CPython module of the rotation and shared-prefix calls, on this library."""
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise ImportError(f"{_PKG}/_binding.so is missing or stale: build it with `python "
+                          "paged_kv_cache_476_b200/build.py`") from e
+    _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        _lib.pkv_qk_norm_rope, _lib.paged_kv_append_rope, _lib.paged_decode_attention_shared)),
+        PagedKVError)
+    return _binding
+
+
+_binding = _load_binding()
 
 
 def _check(what: str, status: int):
@@ -542,7 +543,8 @@ def paged_kv_append_rope(cache: PagedKVCache, rope: Rope, page_table, seq_lens_b
     def call(s):
         out = None if q is None else _result("q_out", q_out, q, q.shape)
         _check("paged_kv_append_rope", _lib.paged_kv_append_rope(
-            cache._ref, rope._ref, page_table.data_ptr(), max_pages, seq_lens_before.data_ptr(), cu_new_tokens.data_ptr(), B, T,
+            cache._ref, rope._ref, page_table.data_ptr(), max_pages,
+            seq_lens_before.data_ptr(), cu_new_tokens.data_ptr(), B, T,
             k_new.data_ptr(), ks, v_new.data_ptr(), vs, None if q is None else q.data_ptr(), qs,
             Hq, None if q is None else out.data_ptr(),
             None if positions is None else positions.data_ptr(), s))

@@ -5,8 +5,10 @@
 // Each function takes what the wrapper of the same name has been given, for
 // results that the call allocates, on the current stream and device.  It returns
 // NotImplemented for everything it does not find in order (an argument to
-// refuse, another device, a status other than PKV_OK), without having launched
-// anything: the wrapper then goes the long way, which says what is wrong.
+// refuse, another device, a status of the host's checks), without having launched
+// anything: the wrapper then goes the long way, which says what is wrong.  A CUDA
+// error may come behind a launch, so it is raised here and nothing is done twice;
+// for the same reason the results are whole Python objects before the call.
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -21,6 +23,7 @@ namespace {
 decltype(&pkv_qk_norm_rope) c_norm_rope;
 decltype(&paged_kv_append_rope) c_append_rope;
 decltype(&paged_decode_attention_shared) c_shared;
+PyObject* error_class;  // PagedKVError(what, status)
 
 PyObject* not_handled() { Py_RETURN_NOTIMPLEMENTED; }
 
@@ -84,6 +87,35 @@ struct CacheArgs {
 
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream(dev).stream(); }
 
+// An object that goes with its owner unless it is released as the result.
+struct Result {
+  PyObject* o = nullptr;
+  explicit Result(PyObject* x) : o(x) {}
+  ~Result() { Py_XDECREF(o); }
+  PyObject* release() {
+    PyObject* x = o;
+    o = nullptr;
+    return x;
+  }
+};
+
+PyObject* wrap(const at::Tensor& t) { return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None); }
+
+PyObject* wrap2(const at::Tensor& a, const at::Tensor& b) {
+  Result x(wrap(a)), y(wrap(b));
+  return x.o && y.o ? PyTuple_Pack(2, x.o, y.o) : nullptr;
+}
+
+// The call's answer, by its status.
+PyObject* answer(const char* what, int status, Result& result) {
+  if (status == PKV_OK) return result.release();
+  if (status != PKV_ERR_CUDA) return not_handled();  // nothing was launched
+  PyObject* e = PyObject_CallFunction(error_class, "si", what, status);
+  if (e) PyErr_SetObject(error_class, e);
+  Py_XDECREF(e);
+  return nullptr;
+}
+
 at::Tensor like(const at::Tensor& t, at::IntArrayRef sizes) { return at::empty(sizes, t.options()); }
 
 // rope, q, k, positions, error_flags
@@ -114,17 +146,14 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   at::Tensor qo, ko;
   if (q.t) qo = like(*q.t, q.t->sizes());
   if (k.t) ko = like(*k.t, k.t->sizes());
+  Result out(wrap2(qo, ko));
+  if (!out.o) return nullptr;
   const int st = c_norm_rope(
       r.rope, q.data(), q.stride, (int32_t)q.heads, k.data(), k.stride, (int32_t)k.heads,
       (int32_t)x.dim, pos ? pos->data_ptr<int32_t>() : nullptr, (int32_t)x.tokens,
       q.t ? qo.data_ptr() : nullptr, k.t ? ko.data_ptr() : nullptr,
       flags ? flags->data_ptr<int32_t>() : nullptr, stream_of(dev));
-  if (st != PKV_OK) return not_handled();
-  PyObject* out = PyTuple_New(2);
-  if (!out) return nullptr;
-  PyTuple_SET_ITEM(out, 0, q.t ? THPVariable_Wrap(std::move(qo)) : Py_NewRef(Py_None));
-  PyTuple_SET_ITEM(out, 1, k.t ? THPVariable_Wrap(std::move(ko)) : Py_NewRef(Py_None));
-  return out;
+  return answer("pkv_qk_norm_rope", st, out);
 }
 
 // cache, rope, page_table, seq_lens_before, cu_new_tokens, k_new, v_new, q, positions,
@@ -158,14 +187,14 @@ PyObject* append_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   at::Tensor out;
   if (q.t) out = like(*q.t, q.t->sizes());
+  Result result(wrap(out));
+  if (!result.o) return nullptr;
   const int st = c_append_rope(
       c.cache, r.rope, table->data_ptr<int32_t>(), (int32_t)table->size(1),
       before->data_ptr<int32_t>(), cu->data_ptr<int32_t>(), (int32_t)batch, (int32_t)total,
       k.data(), k.stride, v.data(), v.stride, q.data(), q.stride, (int32_t)q.heads,
       q.t ? out.data_ptr() : nullptr, pos ? pos->data_ptr<int32_t>() : nullptr, stream_of(dev));
-  if (st != PKV_OK) return not_handled();
-  if (!q.t) Py_RETURN_NONE;
-  return THPVariable_Wrap(std::move(out));
+  return answer("paged_kv_append_rope", st, result);
 }
 
 // cache, q, page_table, seq_lens, max_seq_len, cu_groups, prefix_lens, softmax_scale,
@@ -200,18 +229,15 @@ PyObject* decode_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bool want_lse = PyObject_IsTrue(a[9]) == 1;
   at::Tensor out = like(*q, q->sizes()), lse;
   if (want_lse) lse = at::empty({batch, heads}, q->options().dtype(at::kFloat));
+  Result result(wrap2(out, lse));
+  if (!result.o) return nullptr;
   const int st = c_shared(
       c.cache, q->data_ptr(), (int32_t)heads, (int32_t)(heads / c.cache->num_kv_heads),
       table->data_ptr<int32_t>(), (int32_t)table->size(1), lens->data_ptr<int32_t>(),
       (int32_t)batch, (int32_t)max_len, cu->data_ptr<int32_t>(), prefix->data_ptr<int32_t>(),
       (int32_t)groups, (float)scale, out.data_ptr(), want_lse ? lse.data_ptr<float>() : nullptr,
       work.data_ptr(), work.nbytes(), stream_of(dev));
-  if (st != PKV_OK) return not_handled();
-  PyObject* res = PyTuple_New(2);
-  if (!res) return nullptr;
-  PyTuple_SET_ITEM(res, 0, THPVariable_Wrap(std::move(out)));
-  PyTuple_SET_ITEM(res, 1, want_lse ? THPVariable_Wrap(std::move(lse)) : Py_NewRef(Py_None));
-  return res;
+  return answer("paged_decode_attention_shared", st, result);
 }
 
 // C++ exceptions (an allocation that fails, before any launch): the wrapper meets
@@ -225,14 +251,16 @@ PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   }
 }
 
-// Addresses of the three entry points in libpagedkv.so, as the package loaded it.
+// Addresses of the three entry points in libpagedkv.so, as the package loaded it, and
+// the class of its errors.
 PyObject* bind(PyObject*, PyObject* args) {
-  PyObject *x, *y, *z;
-  if (!PyArg_ParseTuple(args, "OOO", &x, &y, &z)) return nullptr;
+  PyObject *x, *y, *z, *e;
+  if (!PyArg_ParseTuple(args, "OOOO", &x, &y, &z, &e)) return nullptr;
   c_norm_rope = reinterpret_cast<decltype(c_norm_rope)>(PyLong_AsVoidPtr(x));
   c_append_rope = reinterpret_cast<decltype(c_append_rope)>(PyLong_AsVoidPtr(y));
   c_shared = reinterpret_cast<decltype(c_shared)>(PyLong_AsVoidPtr(z));
   if (PyErr_Occurred()) return nullptr;
+  Py_XSETREF(error_class, Py_NewRef(e));
   Py_RETURN_NONE;
 }
 
