@@ -21,6 +21,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import warnings
 from typing import Optional
 
 import numpy as np
@@ -205,13 +206,30 @@ class PagedKVError(RuntimeError):
         self.status = status
 
 
+class _NoBinding:
+    """In place of the CPython module: every call goes the long way."""
+
+    norm_rope = append_rope = decode_shared = staticmethod(lambda *args: NotImplemented)
+
+
 def _load_binding():
-    """The CPython module of the rotation and shared-prefix calls, on this library."""
+    """The CPython module of the rotation and shared-prefix calls, on this library.
+
+    It is a short way to the library and no more: where it is missing, or was
+    built against another torch or Python, the same calls go through ctypes.
+    """
+    from .build import binding_key
+
     try:
         from . import _binding
+
+        if _binding.KEY != binding_key():
+            raise ImportError(f"built against {_binding.KEY}, this is {binding_key()}")
     except ImportError as e:
-        raise ImportError(f"{_PKG}/_binding.so is missing or stale: build it with `python "
-                          "paged_kv_cache_476_b200/build.py`") from e
+        warnings.warn(f"{_PKG}/_binding.so cannot be used ({e}): small rotation and shared-prefix "
+                      "calls take about 15 us longer; build it again with `python "
+                      "paged_kv_cache_476_b200/build.py`", RuntimeWarning)
+        return _NoBinding
     _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         _lib.pkv_qk_norm_rope, _lib.paged_kv_append_rope, _lib.paged_decode_attention_shared)),
         PagedKVError)

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import subprocess
@@ -53,6 +54,13 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _read(path):
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
 def _compile(src, extra):
     obj = os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".o")
     if _stale(obj, [src, *_headers()]) or extra.get("force"):
@@ -67,10 +75,16 @@ def _compile(src, extra):
     return obj, ""
 
 
+def binding_key() -> str:
+    """What the CPython module is built against: it reads tensors through torch's inline
+    code, so it goes with one torch and one Python."""
+    return (f"torch {importlib.metadata.version('torch')}, "
+            f"{sysconfig.get_config_var('SOABI') or sys.version}")
+
+
 def _build_binding(force):
-    """The CPython module; torch is located without importing it."""
-    if not (force or _stale(BINDING, [BINDING_SRC, *_headers()])):
-        return
+    """The CPython module; torch is located without importing it.  It carries its key and
+    is built again where that or the command changes (kept beside the objects)."""
     torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     tmp = BINDING + f".tmp{os.getpid()}"
     dirs = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
@@ -78,12 +92,18 @@ def _build_binding(force):
             os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
             sysconfig.get_paths()["include"]]
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-Wall", "-shared", *(f"-I{d}" for d in dirs),
-           BINDING_SRC, "-o", tmp, "-L" + os.path.join(torch, "lib"), "-ltorch_python",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+           f'-DPKV_BINDING_KEY="{binding_key()}"', BINDING_SRC, "-L" + os.path.join(torch, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    made_by = os.path.join(BUILD, "binding.cmd")
+    want = "\n".join(cmd)
+    if not force and not _stale(BINDING, [BINDING_SRC, *_headers()]) and _read(made_by) == want:
+        return
+    r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(made_by, "w") as f:
+        f.write(want)
 
 
 def build(force: bool = False, verbose: bool = False, flags=()) -> str:

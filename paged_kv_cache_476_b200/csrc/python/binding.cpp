@@ -280,4 +280,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding(void) { return PyModule_Create(&module); }
+// KEY: the torch and Python this was built against; the package binds no other.
+PyMODINIT_FUNC PyInit__binding(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "KEY", PKV_BINDING_KEY) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
