@@ -16,6 +16,7 @@ import glob
 import importlib.metadata
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -61,6 +62,26 @@ def _read(path):
         return f.read()
 
 
+def check_registers(source: str, log: str) -> None:
+    """Kernels that exchange registers (setmaxnreg) count on what their block is launched
+    with, ``kLaunchRegs`` in the source, of a compiler that is free to allot fewer: an
+    exchange that asks for more than the block has would wait for ever.  The launch
+    refuses such a kernel; this says so where it can be acted on.  ``log`` is what
+    ptxas -v prints."""
+    want = re.search(r"\bkLaunchRegs = (\d+)", source)
+    if not want:
+        return
+    kernels = re.findall(r"Compiling entry function '(\S*prefix_kernel\S*)'.*?Used (\d+) registers",
+                         log, re.S)
+    quantised = [(k, int(n)) for k, n in kernels if not re.search(r"prefix_kernelILi\d+ELi0E", k)]
+    if not quantised:
+        raise RuntimeError("no registers of the quantised prefix kernels in the compiler's output")
+    for kernel, n in quantised:
+        if n < int(want[1]):
+            raise RuntimeError(f"{kernel} was compiled to {n} registers, its register exchange "
+                               f"counts on {want[1]} (kLaunchRegs, with the split beside it)")
+
+
 def _compile(src, extra):
     obj = os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".o")
     if _stale(obj, [src, *_headers()]) or extra.get("force"):
@@ -68,9 +89,18 @@ def _compile(src, extra):
             cmd = [CXX, *CXXFLAGS, "-c", src, "-o", obj]
         else:
             cmd = [NVCC, *ARCH, *FLAGS, *extra.get("flags", []), "-c", src, "-o", obj]
+            source = _read(src)
+            if "kLaunchRegs" in source and "-v" not in cmd:
+                cmd += ["-Xptxas", "-v"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        if src.endswith(".cu"):
+            try:
+                check_registers(source, r.stdout + r.stderr)
+            except RuntimeError:
+                os.unlink(obj)
+                raise
         return obj, r.stderr
     return obj, ""
 
