@@ -211,9 +211,9 @@ static bool prefix_plan(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads
 }
 
 // Bytes of the prefix partials, behind the decode workspace.
-static size_t prefix_bytes(int32_t rows, int32_t units, int32_t head_dim) {
+static size_t prefix_bytes(int32_t rows, int32_t units, int32_t groups, int32_t head_dim) {
   return (size_t)rows * head_dim * sizeof(float) + round16((size_t)rows * sizeof(float2)) +
-         (size_t)units * sizeof(int4);
+         (size_t)units * sizeof(int4) + (size_t)groups * sizeof(Span);
 }
 
 }  // namespace pkv
@@ -392,7 +392,7 @@ size_t paged_decode_shared_workspace_bytes(int32_t batch, int32_t num_q_heads,
       !prefix_plan(batch, num_q_heads, num_kv_heads, max_seq_len, num_groups, sms, &ctas, &rows))
     return 0;
   if (num_groups == 0) return own;
-  const size_t n = own + prefix_bytes(rows, batch * num_kv_heads, head_dim);
+  const size_t n = own + prefix_bytes(rows, batch * num_kv_heads, num_groups, head_dim);
   return (n + 255) & ~size_t(255);
 }
 
@@ -517,6 +517,7 @@ static int decode_entry(const pkv_cache* cache, const void* q, int32_t num_q_hea
     sp.pre_ml = reinterpret_cast<float2*>(pre);
     pre += round16((size_t)sp.pre_rows * sizeof(float2));
     sp.pre_info = reinterpret_cast<int4*>(pre);
+    sp.spans = reinterpret_cast<Span*>(pre + units * sizeof(int4));
     CUtensorMap tq;
     if ((st = encode_q_map(&tq, q, batch, num_q_heads, D, gqa_group))) return st;
     e = shared_prefix_run(D, fmt, tq, tk, tv, sp, pre_ctas, s);

@@ -373,10 +373,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   // With shared prefixes a length takes a search among the groups: every thread
   // of the CTA makes some, once.
   const int32_t* lens = nullptr;
+  const Span* spans = nullptr;
   constexpr int kPlanned = kStages * Ly::kStageB / 4;  // in place of the tiles
   if (kGroups && p.batch <= kPlanned) {
     int32_t* made = reinterpret_cast<int32_t*>(tiles);
+    Span* made_spans = reinterpret_cast<Span*>(made + ((p.batch + 3) & ~3));
+    if (p.num_groups <= (kPlanned - ((p.batch + 3) & ~3)) / 4) {
+      plan_spans(p, made_spans, nullptr, warp, kThreads / 32, lane);
+      spans = made_spans;
+    }
     for (int b = threadIdx.x; b < p.batch; b += kThreads) made[b] = own_len<kGroups>(p, b, c == 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
     lens = made;
   }
@@ -401,7 +408,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     // With shared prefixes, as many as fit the SMs that the prefix kernel leaves
     // (a few tiles are one each wherever they run).
     if (kGroups && T > p.num_sms) {
-      const int sms = p.num_sms - divide_sms<kFmt>(p, lane).prefix_sms;
+      const Division dv = divide_sms<kFmt, true>(p, spans, unshared_cost<kFmt>(p, lane), lane);
+      const int sms = p.num_sms - dv.prefix_sms;
       Ce = min(Ce, (int64_t)max(1, sms * p.ctas_per_sm));
     }
     if (c < Ce) {
@@ -678,8 +686,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       __syncwarp();
       ++issued;
-      // advance to the next tile of the work list (past the unit's end cost)
-      if (++t == ntile) {
+      // advance to the next tile of the work list (past the unit's end cost), if there is
+      // one: a search through the empty sequences behind the last is long
+      if (++t == ntile && i + 1 < n_tiles) {
         t = 0;
         x += unit_end_cost<kFmt>();
         if (++g == Hkv) {

@@ -36,6 +36,92 @@ __device__ __forceinline__ int32_t shared_tokens(const DecodeParams& p, int b, i
   return len >= n ? n : 0;
 }
 
+// Where a group's prefix is held.  Only members that hold the whole prefix share it,
+// so its rows go from the first such member (whose table row names the pages) to the
+// last: shorter members and padded rows at a group's ends cost nothing.  All 0 where
+// nobody holds it.  Warp-wide.
+__device__ __forceinline__ Span group_span(const DecodeParams& p, int g, int lane) {
+  Span s = {0, 0, 0, 0};
+  const int32_t n = group_tokens(p, g);
+  if (n == 0) return s;
+  const int32_t b0 = __ldg(p.cu_groups + g), b1 = __ldg(p.cu_groups + g + 1);
+#pragma unroll 1
+  for (int base = b0; base < b1; base += 32) {
+    const int b = base + lane;
+    const uint32_t hit =
+        __ballot_sync(0xffffffffu, b < b1 && __ldg(p.seq_lens + min(b, b1 - 1)) >= n);
+    if (hit == 0) continue;
+    if (s.holders == 0) s.b0 = base + __ffs(hit) - 1;
+    s.b1 = base + 32 - __clz(hit);
+    s.holders += __popc(hit);
+    s.prefix = n;
+  }
+  return s;
+}
+
+// The span of group base + lane (of none past the last): small groups a lane each,
+// larger ones by the warp.  Warp-wide.
+__device__ __forceinline__ Span make_span(const DecodeParams& p, int base, int lane) {
+  Span mine = {0, 0, 0, 0};
+  const int g = base + lane;
+  const int32_t n = g < p.num_groups ? group_tokens(p, g) : 0;
+  bool large = false;
+  if (n > 0) {
+    const int32_t b0 = __ldg(p.cu_groups + g), b1 = __ldg(p.cu_groups + g + 1);
+    large = b1 - b0 > 32;
+    if (!large) {
+#pragma unroll 4
+      for (int b = b0; b < b1; ++b) {
+        if (__ldg(p.seq_lens + b) < n) continue;
+        if (mine.holders == 0) mine.b0 = b;
+        mine.b1 = b + 1;
+        ++mine.holders;
+        mine.prefix = n;
+      }
+    }
+  }
+#pragma unroll 1
+  for (uint32_t todo = __ballot_sync(0xffffffffu, large); todo; todo &= todo - 1) {
+    const int l = __ffs(todo) - 1;
+    const Span s = group_span(p, base + l, lane);
+    if (l == lane) mine = s;
+  }
+  return mine;
+}
+
+// All groups' spans to `a` and `b` (either may be null), by `warps` warps together.
+__device__ __forceinline__ void plan_spans(const DecodeParams& p, Span* a, Span* b, int warp,
+                                           int warps, int lane) {
+  if (p.num_groups <= 4 * warps) {  // a warp each
+#pragma unroll 1
+    for (int g = warp; g < p.num_groups; g += warps) {
+      const Span s = group_span(p, g, lane);
+      if (lane == 0 && a) a[g] = s;
+      if (lane == 0 && b) b[g] = s;
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int base = 32 * warp; base < p.num_groups; base += 32 * warps) {
+    const Span s = make_span(p, base, lane);
+    if (base + lane < p.num_groups) {
+      if (a) a[base + lane] = s;
+      if (b) b[base + lane] = s;
+    }
+  }
+}
+
+// The span of group base + lane: as planned, or (kMake, null) made here.  Warp-wide.
+template <bool kMake>
+__device__ __forceinline__ Span span_of(const DecodeParams& p, const Span* spans, int base,
+                                        int lane) {
+  if (kMake && !spans) return make_span(p, base, lane);
+  Span mine = {0, 0, 0, 0};
+  if (base + lane < p.num_groups)
+    *reinterpret_cast<int4*>(&mine) = *reinterpret_cast<const int4*>(spans + base + lane);
+  return mine;
+}
+
 // A group's prefix work for one kv head: key tiles of 128, Q tiles of 128
 // rows; a step is one of the one against one of the other.
 struct GroupWork {
@@ -43,13 +129,13 @@ struct GroupWork {
   int64_t steps;
 };
 
-__device__ __forceinline__ GroupWork group_work(const DecodeParams& p, int g) {
+__device__ __forceinline__ GroupWork group_work(const DecodeParams& p, const Span& s) {
   GroupWork w;
-  w.b0 = __ldg(p.cu_groups + g);
-  w.b1 = __ldg(p.cu_groups + g + 1);
-  w.prefix = group_tokens(p, g);
+  w.b0 = s.b0;
+  w.b1 = s.b1;
+  w.prefix = s.prefix;
   w.tiles = (w.prefix + 127) / 128;
-  w.q_tiles = w.prefix > 0 ? ((w.b1 - w.b0) * p.group + 127) / 128 : 0;
+  w.q_tiles = ((w.b1 - w.b0) * p.group + 127) / 128;
   w.steps = (int64_t)w.tiles * w.q_tiles;
   return w;
 }
@@ -95,25 +181,34 @@ __device__ __forceinline__ int64_t warp_sum(int64_t x) {
   return x;
 }
 
-// Warp-wide.
+// What the decode kernel would have to read if nothing were shared, a lane's part of
+// the batch.
 template <int kFmt>
-__device__ Division divide_sms(const DecodeParams& p, int lane) {
-  float own = 0.f, pre = 0.f;
-  int64_t steps = 0, tiles = 0;
-  bool two = false;
+__device__ __forceinline__ float unshared_cost(const DecodeParams& p, int lane) {
+  float own = 0.f;
   const int32_t cap = p.max_pages * p.page_size;
 #pragma unroll 1
   for (int b = lane; b < p.batch; b += 32) {
     const int32_t len = max(0, min(__ldg(p.seq_lens + b), cap));
     if (len > 0) own += (float)((len + 127) / 128) * own_tile_cost<kFmt>() + own_unit_cost<kFmt>();
   }
+  return own;
+}
+
+// Warp-wide, from the lanes' unshared_cost; a prefix saves its holders' tiles.
+template <int kFmt, bool kMake>
+__device__ Division divide_sms(const DecodeParams& p, const Span* spans, float own, int lane) {
+  float pre = 0.f;
+  int64_t steps = 0, tiles = 0;
+  bool two = false;
 #pragma unroll 1
-  for (int g = lane; g < p.num_groups; g += 32) {
-    const GroupWork w = group_work(p, g);
+  for (int base = 0; base < p.num_groups; base += 32) {
+    const Span s = span_of<kMake>(p, spans, base, lane);
+    const GroupWork w = group_work(p, s);
     steps += w.steps;
     tiles += (int64_t)w.tiles * ((w.q_tiles + 1) >> 1);
     two |= w.q_tiles > 1;
-    own -= (float)(w.q_tiles > 0 ? w.b1 - w.b0 : 0) * w.tiles * own_tile_cost<kFmt>();
+    own -= (float)s.holders * w.tiles * own_tile_cost<kFmt>();
     pre += w.tiles * ((w.q_tiles >> 1) * prefix_tile_cost<kFmt>(true) +
                       (w.q_tiles & 1) * prefix_tile_cost<kFmt>(false)) +
            ((w.q_tiles + 1) >> 1) * prefix_unit_cost<kFmt>();

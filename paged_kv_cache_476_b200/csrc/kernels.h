@@ -94,12 +94,19 @@ struct DecodeParams {
   float scale_log2;  // softmax_scale * log2(e)
 };
 
+// Shared prefixes: the members of a group from the first that holds the whole prefix to
+// the last, how many hold it, and its tokens; all 0 where nothing is shared.
+struct __align__(16) Span {
+  int32_t b0, b1, holders, prefix;
+};
+
 // Shared-prefix attention: the partials of the prefix kernel.
 struct SharedParams {
   DecodeParams d;    // the whole call; its partials hold the sequences' own tokens
   float* pre_o;      // prefix partials: float4 vectors, see shared.cu
   float2* pre_ml;    // (max, sum) of each partial row
   int4* pre_info;    // [batch * num_kv_heads]: where a unit's prefix partials are
+  Span* spans;       // [num_groups], by the prefix kernel (every CTA writes the same)
   int32_t pre_rows;  // rows that pre_o and pre_ml hold
   int32_t own_slots; // partial slots of d (of group rows each)
 };

@@ -197,10 +197,10 @@ struct Split {
   }
 };
 
-// Position in the work list: group, head, pair of Q tiles, key tile.
+// Position in the work list: group's work, head, pair of Q tiles, key tile.
 struct Cursor {
   GroupWork w;
-  int32_t g, head, pair, tile;
+  int32_t head, pair, tile;
   int64_t item_x;  // step index of the item's first step
 };
 
@@ -211,12 +211,12 @@ __device__ __forceinline__ int pair_tiles(const GroupWork& w, int pair) {
 
 // Warp-wide: the tile that step x belongs to (x < T); tiles go to the range
 // that holds their last step.
-__device__ Cursor locate(const DecodeParams& p, int64_t x, int lane) {
+__device__ Cursor locate(const DecodeParams& p, const Span* spans, int64_t x, int lane) {
   Cursor c;
   int64_t run = 0;
   for (int base = 0; base < p.num_groups; base += 32) {
-    const int g = base + lane;
-    const int64_t s = g < p.num_groups ? group_work(p, g).steps * p.num_kv_heads : 0;
+    Span mine = span_of<false>(p, spans, base, lane);
+    const int64_t s = group_work(p, mine).steps * p.num_kv_heads;
     int64_t incl = s;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -227,8 +227,10 @@ __device__ Cursor locate(const DecodeParams& p, int64_t x, int lane) {
     if (run + all > x) {
       const int l0 = __ffs(__ballot_sync(0xffffffffu, run + incl > x)) - 1;
       const int64_t before = run + __shfl_sync(0xffffffffu, incl - s, l0);
-      c.g = base + l0;
-      c.w = group_work(p, c.g);
+      mine.b0 = __shfl_sync(0xffffffffu, mine.b0, l0);
+      mine.b1 = __shfl_sync(0xffffffffu, mine.b1, l0);
+      mine.prefix = __shfl_sync(0xffffffffu, mine.prefix, l0);
+      c.w = group_work(p, mine);
       int64_t off = x - before;
       c.head = (int)quotient(off, c.w.steps);
       off -= c.head * c.w.steps;
@@ -240,8 +242,7 @@ __device__ Cursor locate(const DecodeParams& p, int64_t x, int lane) {
     }
     run += all;
   }
-  c.g = p.num_groups;  // not reached for x < T
-  c.w = GroupWork{};
+  c.w = GroupWork{};  // not reached for x < T
   c.head = c.pair = c.tile = 0;
   c.item_x = run;
   return c;
@@ -254,18 +255,6 @@ __device__ void check_groups(const DecodeParams& p, int lane) {
     if (b0 < 0 || b1 < b0 || b1 > p.batch || __ldg(p.prefix_lens + g) < 0)
       flag_error(p.flags, PKV_FLAG_BAD_LENGTH);
   }
-}
-
-// First sequence of a group that holds the whole prefix, whose table row names
-// the prefix's pages; -1: none does.  Warp-wide.
-__device__ int first_holder(const DecodeParams& p, const GroupWork& w, int lane) {
-  for (int base = w.b0; base < w.b1; base += 32) {
-    const int b = base + lane;
-    const uint32_t hit =
-        __ballot_sync(0xffffffffu, b < w.b1 && __ldg(p.seq_lens + min(b, w.b1 - 1)) >= w.prefix);
-    if (hit) return base + __ffs(hit) - 1;
-  }
-  return -1;
 }
 
 // A landed tile of codes to f16 (exact: every E4M3 and INT8 value is one, and an
@@ -460,9 +449,22 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
   Split split{1, 0};
   int64_t x = 0, x_end = 0;
   Cursor cur{};
-  int b_table = -1;
+  // The groups' spans: for the start in place of the first tiles where they fit, for
+  // later segments in the workspace.  By the warps that set nothing else up, with a
+  // barrier of their own and the scheduler's (which would wait 1 us for the others).
+  Span* const near = p.num_groups <= (int)(2 * Sm::kStageB / sizeof(Span))
+                         ? reinterpret_cast<Span*>(skv) : nullptr;
+  constexpr int kPlanWarp0 = 2, kPlanWarps = 6;
+  constexpr int kPlanners = (kPlanWarps + 1) * 32;  // with the scheduler
+  if (warp >= kPlanWarp0 && warp < kPlanWarp0 + kPlanWarps) {
+    plan_spans(p, near, sp.spans, warp - kPlanWarp0, kPlanWarps, lane);
+    asm volatile("bar.arrive 1, %0;" ::"n"(kPlanners) : "memory");
+  }
   if (warp == kSchedWarp) {
-    const Division dv = divide_sms<kFmt>(p, lane);
+    const float unshared = unshared_cost<kFmt>(p, lane);
+    asm volatile("bar.sync 1, %0;" ::"n"(kPlanners) : "memory");
+    const Span* spans = near ? near : sp.spans;
+    const Division dv = divide_sms<kFmt, false>(p, spans, unshared, lane);
     const int64_t T = dv.steps;
     // Every range holds a whole tile (two steps of an item with two Q tiles).
     const int64_t most = min((int)gridDim.x, dv.prefix_sms);
@@ -474,16 +476,16 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       x_end = split.begin(blockIdx.x + 1);
     }
     if (x < x_end) {
-      cur = locate(p, x, lane);
-      b_table = first_holder(p, cur.w, lane);
+      cur = locate(p, spans, x, lane);
       // the producer's first page ids
       const int64_t key0 = (int64_t)cur.tile * kKeys + lane * 64;
-      if (b_table >= 0 && key0 < cur.w.prefix)
+      if (key0 < cur.w.prefix)
         asm volatile("prefetch.global.L1 [%0];" ::"l"(
-            p.page_table + (int64_t)b_table * p.max_pages + key0 / p.page_size));
+            p.page_table + (int64_t)cur.w.b0 * p.max_pages + key0 / p.page_size));
     }
     if (lane == 0) ct.idle = x < x_end ? 0 : 1;
   }
+  fence_async_smem();  // (the spans' place is the loads' from here on)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -687,15 +689,12 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
       while (true) {
         Segment s{};
         if (x < x_end) {
-          if (!first) {
-            cur = locate(p, x, lane);
-            b_table = first_holder(p, cur.w, lane);
-          }
+          if (!first) cur = locate(p, sp.spans, x, lane);
           first = false;
           const int w = pair_tiles(cur.w, cur.pair);
           s.b0 = cur.w.b0 + cur.pair * 2 * TQ;
           s.b1 = min(cur.w.b1, s.b0 + 2 * TQ);
-          s.b_table = b_table;
+          s.b_table = cur.w.b0;
           s.head = cur.head;
           s.rows = (s.b1 - s.b0) * G;
           s.prefix = cur.w.prefix;
@@ -703,7 +702,6 @@ __global__ void __launch_bounds__(Smem<D, kFmt>::kThreads, 1)
           // tiles whose last step lies before the range's end
           const int64_t left = x_end - cur.item_x;
           s.n = (int)min((int64_t)cur.w.tiles, w == 2 ? left >> 1 : left) - s.tile0;
-          if (b_table < 0) s.n = 0;  // nobody to read the result
           // Items of one CTA lie 2 * rows apart, parts of an item kPairRows: no two
           // segments overlap, and the last ends by 2 * batch * heads + kPairRows * CTAs.
           const int64_t base = 2 * ((int64_t)p.num_kv_heads * cur.w.b0 * G +
