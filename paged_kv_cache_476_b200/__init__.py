@@ -309,7 +309,10 @@ def _on(device: torch.device, stream, call):
     if stream is None and device.index == torch.cuda.current_device():
         return call(_current_raw_stream(device.index))
     if stream is not None and not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device)
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        # (a handle of 0 is the default stream, which ExternalStream takes for none)
+        stream = (torch.cuda.ExternalStream(raw, device) if raw
+                  else torch.cuda.default_stream(device))
     if stream is not None and stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
