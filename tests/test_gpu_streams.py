@@ -21,14 +21,14 @@ class _Handle:
 def test_the_call_goes_to_the_stream_that_is_given(pkv):
     dev = torch.device("cuda", torch.cuda.current_device())
     side = torch.cuda.Stream()
-    on = lambda stream: pkv._on(dev, stream, lambda raw: (raw, torch.cuda.current_stream()))
+    on = lambda stream: pkv._on(dev, stream, lambda raw: (raw, torch.cuda.current_stream().cuda_stream))
     for given in (side, side.cuda_stream, _Handle(side.cuda_stream)):
         raw, current = on(given)
-        assert raw == side.cuda_stream and current == side
+        assert raw == side.cuda_stream and current == raw
     for given in (0, torch.cuda.default_stream(), torch.cuda.default_stream().cuda_stream, _Handle(0)):
         with torch.cuda.stream(side):
             raw, current = on(given)
-        assert raw == 0 and current == torch.cuda.default_stream()
+        assert raw == 0 and current == 0
     with torch.cuda.stream(side):
         assert on(None)[0] == side.cuda_stream
 
