@@ -967,6 +967,18 @@ class StepDriver:
         n = nd + nc
         if n == 0 or n > self.max_rows:
             raise ValueError(f"a step needs 1..{self.max_rows} rows, got {n}")
+        if self.rope is not None:  # before the allocator counts the step's tokens as stored
+            total = nd + int(sum(chunk_lens))
+            heads = self.cache.num_kv_heads
+            for name, t in (("k_new", k_new), ("v_new", v_new), ("q", q)):
+                _rows(name, t)
+                _same_device(self.cache.k_pool.device, **{name: t})
+                if t.shape[0] < total or t.shape[2] != self.cache.head_dim:
+                    raise ValueError(f"{name} must hold the step's {total} tokens, with head_dim "
+                                     f"{self.cache.head_dim}")
+            if k_new.shape != v_new.shape or k_new.shape[1] != heads or q.shape[1] % heads:
+                raise ValueError(f"k_new and v_new must have {heads} heads, q a multiple of them")
+            self.rope._check(self.cache.head_dim, self.cache.k_pool.device)
         mp = self.alloc.max_pages_per_seq
         self._slots[:nd] = decode_slots
         self._slots[nd:n] = chunk_slots
