@@ -407,6 +407,8 @@ def rope_cos_sin(max_positions: int, rotary_dim: int, base: float = 10000.0, inv
     cosines of ``position * inv_freq`` and then the sines, computed in fp64.
     ``inv_freq`` (``[rotary_dim / 2]``) replaces ``base ** (-2i / rotary_dim)``.
     """
+    if rotary_dim < 0 or rotary_dim % 2 or max_positions < 1:
+        raise ValueError("rotary_dim must be even, max_positions positive")
     half = rotary_dim // 2
     if inv_freq is None:
         inv_freq = base ** (-torch.arange(half, dtype=torch.float64) / half)
@@ -472,7 +474,8 @@ def pkv_qk_norm_rope(rope: Rope, q, k, positions=None, q_out=None, k_out=None, e
     of a token are contiguous, tokens may lie apart (slices of a fused
     projection).  ``q_out`` may be ``q`` itself where that is contiguous.
     Returns ``(q_out, k_out)``; rows of tokens with a position outside the
-    table keep what they held and raise ``PKV_FLAG_BAD_LENGTH``.
+    table keep what they held (in a new result: are undefined) and raise
+    ``PKV_FLAG_BAD_LENGTH``.
     """
     if stream is None and q_out is None and k_out is None:
         r = _binding.norm_rope(rope._args, q, k, positions, error_flags)
@@ -525,7 +528,8 @@ def paged_kv_append_rope(cache: PagedKVCache, rope: Rope, page_table, seq_lens_b
     ``[T]``.  Tokens may lie apart in memory (slices of a fused projection).
     Returns ``q_out`` bf16 ``[T, Hq, D]`` (``q`` itself may be given where it is
     contiguous), None without ``q``.  Tokens behind ``cu_new_tokens[-1]`` (a
-    padded batch) change nothing.
+    padded batch) change nothing: their rows of a given ``q_out`` keep what they
+    held, those of a new one are undefined.
     """
     if stream is None and q_out is None:
         r = _binding.append_rope(cache._args, rope._args, page_table, seq_lens_before,
