@@ -319,6 +319,8 @@ int paged_decode_attention_append(const pkv_cache* cache, const void* q, int32_t
  *   num_groups   0: paged_decode_attention
  *   workspace    paged_decode_shared_workspace_bytes(...) bytes (0 on error, for
  *                the current device), 16-byte aligned; one call at a time may use it
+ * Padded rows (length 0) and members without the whole prefix cost what they read.
+ * Small prefixes are shared too, where paged_decode_attention may be some us faster.
  * Results equal paged_decode_attention's up to the order of summation, and are
  * the same from run to run.  The other arguments, flags and errors are those of
  * paged_decode_attention.

@@ -142,8 +142,9 @@ __device__ __forceinline__ GroupWork group_work(const DecodeParams& p, const Spa
 
 // The two kernels run side by side: prefix CTAs (one per SM) that find no work
 // leave at once, and decode CTAs take their SMs.  Both kernels work out the same
-// division, in SM-microseconds as measured on B200 at D = 128; results do not
-// depend on it.
+// division, in SM-microseconds as measured on B200 at D = 128 with both kernels
+// running (of quantised pools more than the prefix kernel alone takes; used at D = 64
+// too, where a bf16 tile takes 0.65 of it); results do not depend on it.
 struct Division {
   int64_t steps;   // of the prefix kernel
   bool pairs;      // some group has two Q tiles

@@ -13,10 +13,12 @@
 // The prefix kernel.
 //  * Bound: HBM bytes of the prefix for one Q tile of bf16 (1.4 us a 128-key tile
 //    and SM at head_dim 128: the SM's share); the cycle of a slot, its softmax, the
-//    products and the hand-offs between them, for two (2.35 us a tile; 3.0 of
-//    quantised pools); the converters for one Q tile of quantised pools (about 1.4
-//    us, FP4 1.6).  16 sequences behind 65,536 bf16 tokens of 8 kv heads: 54 us, 4.9
-//    TB/s, of which 6 us pass before the first tile has landed.
+//    products and the hand-offs between them, for two (2.35 us a tile; E4M3 2.2, INT8
+//    and FP4 2.5); the converters for one Q tile of quantised pools (E4M3 1.25 us,
+//    INT8 and FP4 1.45).  These are the kernel's alone; beside the decode kernel the
+//    quantised ones take longer (3.0 for two E4M3 tiles).  At head_dim 64: 0.95 and
+//    2.0 (bf16), 1.15 to 1.2 and 2.15.  16 sequences behind 65,536 bf16 tokens of 8 kv
+//    heads: 54 us, 4.9 TB/s, of which 6 us pass before the first tile has landed.
 //  * Items.  A group's rows of one kv head are cut into pairs of 128-row Q
 //    tiles, A and B.  An item is (group, kv head, pair) over the prefix's
 //    128-key tiles.  The items' steps (a tile times one Q tile) in order are
