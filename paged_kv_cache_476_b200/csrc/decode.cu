@@ -377,12 +377,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int kPlanned = kStages * Ly::kStageB / 4;  // in place of the tiles
   if (kGroups && p.batch <= kPlanned) {
     int32_t* made = reinterpret_cast<int32_t*>(tiles);
+    for (int b = threadIdx.x; b < p.batch; b += kThreads) made[b] = own_len<kGroups>(p, b, c == 0);
     Span* made_spans = reinterpret_cast<Span*>(made + ((p.batch + 3) & ~3));
     if (p.num_groups <= (kPlanned - ((p.batch + 3) & ~3)) / 4) {
       plan_spans(p, made_spans, nullptr, warp, kThreads / 32, lane);
       spans = made_spans;
     }
-    for (int b = threadIdx.x; b < p.batch; b += kThreads) made[b] = own_len<kGroups>(p, b, c == 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
     lens = made;
